@@ -1,4 +1,5 @@
-"""Thin Python binding of libgdn_cpr.so (the C ABI in include/gdn_cpr.h).
+"""Thin Python binding of libgdn_cpr.so (the C ABI in include/gdn_cpr.h,
+gdn_pik.h, gdn_qk_norm.h and gdn_glr.h).
 
 Argument marshalling only: torch provides device memory and the current CUDA
 stream; every step of the layer runs in the library's CUDA kernels.  There is
@@ -33,7 +34,12 @@ GDN_DEVERR_CU_SEQLENS = 1
 GDN_DEVERR_POS = 2
 GDN_DEVERR_TIMEOUT = 4
 GDN_BWD_REUSE_FORWARD = 1
+GDN_QK_NORM_L2 = 0
+GDN_QK_NORM_RMS = 1
+GDN_GLR_INPUT_PLAIN = 0
+GDN_GLR_INPUT_COMPLEMENT = 1
 CHUNK = 64
+GLR_CHUNK = 16
 
 
 class GdnError(RuntimeError):
@@ -49,6 +55,12 @@ class DecodeStateStruct(ctypes.Structure):
                 ("buf_beta", ctypes.c_void_p), ("buf_g", ctypes.c_void_p),
                 ("pos", ctypes.c_void_p), ("error", ctypes.c_void_p),
                 ("resync", ctypes.c_void_p), ("n_slots", ctypes.c_int)]
+
+
+class GlrStateStruct(ctypes.Structure):
+    _fields_ = [("h", ctypes.c_void_p), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("error", ctypes.c_void_p),
+                ("n_slots", ctypes.c_int)]
 
 
 def _load() -> ctypes.CDLL:
@@ -95,6 +107,19 @@ def _load() -> ctypes.CDLL:
         "gdn_cpr_contract_check": (i32, [ctypes.c_char_p, i32, i32, i32, i32, i32]),
         "gdn_sha256": (i32, [ctypes.c_char_p, sz, ctypes.c_char_p]),
         "gdn_selftest_bounded_wait": (i32, [i32, vp, vp]),
+        "gdn_qk_norm_forward": (i32, [vp, i64, vp, i64, i32, i64, i32, i32, i32, i32, f32, vp, vp,
+                                      vp, vp, i32, i32, vp, i64, vp, i64, i32, vp]),
+        "gdn_qk_norm_backward_workspace_bytes": (sz, [i64, i32, i32, i32]),
+        "gdn_qk_norm_backward": (i32, [vp, i64, vp, i64, i32, i64, i32, i32, i32, i32, f32, vp,
+                                       vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, vp, i64, vp,
+                                       i64, vp, vp, vp, sz, vp]),
+        "gdn_glr_carry_rows": (i64, [i32, i64]),
+        "gdn_glr_forward": (i32, [vp, i64, i32, vp, i64, i32, vp, i32, i64, i32, i32, vp, vp, i64,
+                                  i32, vp, ctypes.POINTER(GlrStateStruct), vp, vp, vp, vp]),
+        "gdn_glr_backward": (i32, [vp, i64, i32, vp, i64, i32, vp, i32, i64, i32, i32, vp, vp,
+                                   i64, i32, vp, vp, i64, vp, i64, vp, vp, vp]),
+        "gdn_glr_decode_step": (i32, [vp, i64, i32, vp, i64, i32, vp, i32, i32, i32,
+                                      GlrStateStruct, vp, i64, i32, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -445,6 +470,324 @@ def chunk_boundary(s_start, k, v, beta, g, *, s_end=None, stream=None):
                                 _ptr(g), B, H, dk, dv, C, _ptr(s_end), _stream(stream))
     _check(st, "gdn_chunk_boundary")
     return s_end
+
+
+# ---------------------------------------------------------------------------
+# q/k norm and gated linear recurrence (gdn_qk_norm.h, gdn_glr.h)
+# ---------------------------------------------------------------------------
+# These calls take strided rows, run on the device of their tensors (current
+# or not) and check every tensor's shape, dtype and device here, since the C
+# entry points see bare pointers.
+
+class _Call:
+    """Device, stream and checks of one call."""
+
+    def __init__(self, what: str, dev: torch.device, stream):
+        if dev.type != "cuda":
+            raise ValueError("gdn_cpr: tensors must be on a CUDA device (there is no CPU path)")
+        self.what, self.dev = what, dev
+        self.index = dev.index
+        self.user_stream = stream
+        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
+        if self.stream.device_index != self.index:
+            raise ValueError(f"{what}: stream and tensors are on different devices")
+
+    def need(self, ok: bool, why: str):
+        if not ok:
+            raise ValueError(f"{self.what}: {why}")
+
+    def empty(self, shape, dtype):
+        """New memory for an output or scratch, used on the call's stream."""
+        t = torch.empty(shape, dtype=dtype, device=self.dev)
+        if self.user_stream is not None:
+            # the memory may have been freed on the current stream, whose work on it
+            # is waited for; and it is kept from reuse until the call's stream is done
+            self.user_stream.wait_stream(torch.cuda.current_stream(self.dev))
+            t.record_stream(self.user_stream)
+        return t
+
+    def full(self, t, name: str, shape, dtype):
+        """Address of a contiguous tensor (None stays NULL)."""
+        if t is None:
+            return None
+        self.need(t.device == self.dev, f"{name} is on {t.device}, not {self.dev}")
+        self.need(t.dtype == dtype, f"{name} must be {dtype}")
+        self.need(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}")
+        self.need(t.is_contiguous(), f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def rows(self, t, name: str, shape, dtype=None):
+        """Address and row stride of [T, ...] whose rows are contiguous."""
+        self.need(t.device == self.dev, f"{name} is on {t.device}, not {self.dev}")
+        self.need(dtype is None or t.dtype == dtype, f"{name} must be {dtype}")
+        self.need(t.shape == shape, f"{name} must have shape {tuple(shape)}")
+        width = 1
+        for n, step in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+            self.need(n <= 1 or step == width, f"the rows of {name} must be contiguous")
+            width *= n
+        return t.data_ptr(), (t.stride(0) if shape[0] > 1 else width)
+
+    def run(self, fn, *args):
+        if self.index == torch.cuda.current_device():
+            st = fn(*args, self.stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.dev):
+                st = fn(*args, self.stream.cuda_stream)
+        _check(st, self.what)
+
+
+def _dtype_of(code_or_dtype, default):
+    if code_or_dtype is None:
+        return default
+    if code_or_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"gdn_cpr: unsupported dtype {code_or_dtype}")
+    return code_or_dtype
+
+
+def _norm_kind(norm: str) -> int:
+    if norm not in ("l2", "rms"):
+        raise ValueError("norm must be 'l2' or 'rms'")
+    return GDN_QK_NORM_RMS if norm == "rms" else GDN_QK_NORM_L2
+
+
+def _qk_call(what, q, k, norm, wq, wk, positions, inv_freq, stream):
+    some = q if q is not None else k
+    if some is None or any(t is not None and t.dim() != 3 for t in (q, k)):
+        raise ValueError(f"{what}: q, k must be [tokens, heads, d] (one of them may be None)")
+    c = _Call(what, some.device, stream)
+    T, _, d = some.shape
+    Hq = 0 if q is None else q.shape[1]
+    Hk = 0 if k is None else k.shape[1]
+    qp, ldq = (None, 0) if q is None else c.rows(q, "q", (T, Hq, d))
+    kp, ldk = (None, 0) if k is None else c.rows(k, "k", (T, Hk, d), some.dtype)
+    c.need((positions is None) == (inv_freq is None), "positions and inv_freq go together")
+    F = 0
+    if inv_freq is not None:
+        F = inv_freq.numel()
+        c.full(inv_freq, "inv_freq", (F,), torch.float32)
+        c.full(positions, "positions", (T,), torch.int32)
+    head = (qp, ldq, kp, ldk, _dtype_code(some), T, Hq, Hk, d, _norm_kind(norm))
+    tail = (c.full(wq, "wq", (d,), torch.float32), c.full(wk, "wk", (d,), torch.float32),
+            None if F == 0 else positions.data_ptr(), None if F == 0 else inv_freq.data_ptr(),
+            2 * F)
+    return c, some.dtype, (T, Hq, Hk, d), head, tail
+
+
+def qk_norm_forward(q, k, *, norm: str = "l2", eps: float = 1e-6, wq=None, wk=None,
+                    positions=None, inv_freq=None, interleaved: bool = False, out_dtype=None,
+                    oq=None, ok=None, stream=None):
+    """gdn_qk_norm_forward: every head of q [T, Hq, d] and k [T, Hk, d] normalised
+    (norm "l2" or "rms", fp32 weights wq, wk [d] or None) and, with positions [T]
+    int32 and inv_freq [rot_dim / 2] fp32, rotated.  Tokens may be strided; q or
+    k may be None.  oq=q, ok=k works in place.  Returns (oq, ok)."""
+    c, dt, (T, Hq, Hk, d), head, tail = _qk_call("gdn_qk_norm_forward", q, k, norm, wq, wk,
+                                                 positions, inv_freq, stream)
+    given = oq if oq is not None else ok
+    odt = _dtype_of(out_dtype, given.dtype if given is not None else dt)
+    out = []
+    for x, o, H, name in ((q, oq, Hq, "oq"), (k, ok, Hk, "ok")):
+        if x is None:
+            out += [None, None, 0]
+            continue
+        if o is None:
+            o = c.empty((T, H, d), odt)
+        out += [o, *c.rows(o, name, (T, H, d), odt)]
+    c.run(lib.gdn_qk_norm_forward, *head, float(eps), *tail, int(bool(interleaved)), out[1],
+          out[2], out[4], out[5], _dtype_code_of(odt))
+    return out[0], out[3]
+
+
+def qk_norm_backward_workspace_bytes(T: int, Hq: int, Hk: int, d: int) -> int:
+    return int(lib.gdn_qk_norm_backward_workspace_bytes(T, Hq, Hk, d))
+
+
+def qk_norm_backward(q, k, d_oq, d_ok, *, norm: str = "l2", eps: float = 1e-6, wq=None, wk=None,
+                     positions=None, inv_freq=None, interleaved: bool = False,
+                     want_dw: bool = True, grads=None, workspace=None, stream=None):
+    """gdn_qk_norm_backward: q, k and the options of the forward; d_oq, d_ok of
+    one dtype (bf16 or fp32, the fp32 of backward()'s dq and dk for one).  Returns
+    a dict of dq, dk (the dtype of q and k) and dwq, dwk [d] fp32 (None without
+    the weight or want_dw).  Pass ``grads`` (the same dict) to reuse buffers."""
+    c, dt, (T, Hq, Hk, d), head, tail = _qk_call("gdn_qk_norm_backward", q, k, norm, wq, wk,
+                                                 positions, inv_freq, stream)
+    c.need((q is None) == (d_oq is None) and (k is None) == (d_ok is None),
+           "d_oq and d_ok go with q and k")
+    gdt = (d_oq if q is not None else d_ok).dtype
+    gin, gout, res = [], [], {}
+    for s, x, g, H in (("q", q, d_oq, Hq), ("k", k, d_ok, Hk)):
+        if x is None:
+            gin += [None, 0]
+            gout += [None, 0]
+            res["d" + s] = None
+            continue
+        gin += [*c.rows(g, "d_o" + s, (T, H, d), gdt)]
+        dx = grads["d" + s] if grads is not None else c.empty((T, H, d), dt)
+        gout += [*c.rows(dx, "d" + s, (T, H, d), dt)]
+        res["d" + s] = dx
+    for s, w in (("q", wq), ("k", wk)):
+        dw = None
+        if w is not None and want_dw:
+            dw = grads["dw" + s] if grads is not None else c.empty((d,), torch.float32)
+        gout.append(c.full(dw, "dw" + s, (d,), torch.float32))
+        res["dw" + s] = dw
+    need = 0
+    if res["dwq"] is not None or res["dwk"] is not None:
+        need = qk_norm_backward_workspace_bytes(T, Hq, Hk, d)
+        if workspace is None:
+            workspace = c.empty((max(need, 16),), torch.uint8)
+    size = 0
+    if workspace is not None:
+        size = workspace.numel() * workspace.element_size()
+        c.need(workspace.device == c.dev and workspace.is_contiguous(),
+               "workspace must be contiguous and on the device of q and k")
+    c.run(lib.gdn_qk_norm_backward, *head, float(eps), *tail, int(bool(interleaved)), *gin,
+          _dtype_code_of(gdt), *gout, None if workspace is None else workspace.data_ptr(), size)
+    return res
+
+
+def _dtype_code_of(dtype) -> int:
+    if dtype == torch.bfloat16:
+        return GDN_BF16
+    if dtype == torch.float32:
+        return GDN_F32
+    raise ValueError(f"gdn_cpr: unsupported dtype {dtype}")
+
+
+class GlrDecodeState:
+    """Caller-owned decode state (device tensors) of the gated linear recurrence
+    for n_slots sequences; a new one starts every slot from a zero state."""
+
+    def __init__(self, n_slots: int, D: int, device="cuda"):
+        self.n_slots, self.D = n_slots, D
+        f32 = torch.float32
+        self.h = torch.zeros((n_slots, D), dtype=f32, device=device)
+        self.a = torch.ones((n_slots, D), dtype=f32, device=device)
+        self.b = torch.zeros((n_slots, D), dtype=f32, device=device)
+        self.pos = torch.zeros((n_slots,), dtype=torch.int32, device=device)
+        self.error = torch.zeros((1,), dtype=torch.int32, device=device)
+
+    def struct(self) -> GlrStateStruct:
+        return GlrStateStruct(self.h.data_ptr(), self.a.data_ptr(), self.b.data_ptr(),
+                              self.pos.data_ptr(), self.error.data_ptr(), self.n_slots)
+
+    def tensors(self):
+        return (self.h, self.a, self.b, self.pos)
+
+    def clone(self) -> "GlrDecodeState":
+        c = GlrDecodeState.__new__(GlrDecodeState)
+        c.__dict__.update({k: (v.clone() if isinstance(v, torch.Tensor) else v)
+                           for k, v in self.__dict__.items()})
+        return c
+
+
+def _glr_state(c: _Call, state: GlrDecodeState, D: int) -> GlrStateStruct:
+    for name in ("h", "a", "b"):
+        c.full(getattr(state, name), "state." + name, (state.n_slots, D), torch.float32)
+    c.full(state.pos, "state.pos", (state.n_slots,), torch.int32)
+    c.full(state.error, "state.error", (1,), torch.int32)
+    return state.struct()
+
+
+def _glr_inputs(c: _Call, x, g):
+    T, D = x.shape
+    xp, ldx = c.rows(x, "x", (T, D))
+    gp, ldg = c.rows(g, "g", (T, D))
+    return xp, ldx, _dtype_code(x), gp, ldg, _dtype_code(g)
+
+
+def _glr_mode(complement: bool) -> int:
+    return GDN_GLR_INPUT_COMPLEMENT if complement else GDN_GLR_INPUT_PLAIN
+
+
+def _glr_batch(c: _Call, cu_seqlens, n_seqs):
+    N = cu_seqlens.numel() - 1 if n_seqs is None else int(n_seqs)
+    c.need(0 <= N < max(cu_seqlens.numel(), 1), "cu_seqlens has n_seqs + 1 entries")
+    return N, c.full(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32)
+
+
+def glr_carry_rows(n_seqs: int, total_tokens: int) -> int:
+    return int(lib.gdn_glr_carry_rows(n_seqs, total_tokens))
+
+
+def glr_forward(x, g, cu_seqlens, *, n_seqs: Optional[int] = None, h0=None,
+                complement: bool = False, out_dtype=None, h=None, s_final=None,
+                want_state: bool = True, state: Optional[GlrDecodeState] = None, slot_idx=None,
+                carry=None, want_carry: bool = False, error=None, stream=None):
+    """gdn_glr_forward: h_t = exp(g_t) h_{t-1} + x_t for every channel of packed
+    sequences (complement: + (1 - exp(g_t)) x_t).  x, g [T, D], rows may be
+    strided; h0, s_final [N, D] fp32.  ``state`` (and slot_idx) receives the
+    decode state of every sequence; want_carry=True returns the fp32 rows that
+    glr_backward needs.  Returns (h, s_final, carry, error word)."""
+    c = _Call("gdn_glr_forward", x.device, stream)
+    c.need(x.dim() == 2 and g.dim() == 2, "x, g must be [tokens, channels]")
+    T, D = x.shape
+    ins = _glr_inputs(c, x, g)
+    N, cu = _glr_batch(c, cu_seqlens, n_seqs)
+    odt = _dtype_of(out_dtype, h.dtype if h is not None else x.dtype)
+    if h is None:
+        h = c.empty((T, D), odt)
+    hp, ldh = c.rows(h, "h", (T, D), odt)
+    if s_final is None and want_state:
+        s_final = c.empty((N, D), torch.float32)
+    rows = glr_carry_rows(N, T)
+    if carry is None and want_carry:
+        carry = c.empty((rows, D), torch.float32)
+    if error is None:
+        error = c.empty((1,), torch.int32)
+    st = None if state is None else ctypes.byref(_glr_state(c, state, D))
+    c.run(lib.gdn_glr_forward, *ins, cu, N, T, D, _glr_mode(complement),
+          c.full(h0, "h0", (N, D), torch.float32), hp, ldh, _dtype_code_of(odt),
+          c.full(s_final, "s_final", (N, D), torch.float32), st,
+          c.full(slot_idx, "slot_idx", (N,), torch.int32),
+          c.full(carry, "carry", (rows, D), torch.float32),
+          c.full(error, "error", (1,), torch.int32))
+    return h, s_final, carry, error
+
+
+def glr_backward(x, g, cu_seqlens, carry, d_h, *, n_seqs: Optional[int] = None, ds_final=None,
+                 complement: bool = False, want_dh0: bool = True, grads=None, error=None,
+                 stream=None):
+    """gdn_glr_backward: x, g, cu_seqlens and options of the forward that wrote
+    ``carry``; d_h [T, D] (bf16 or fp32).  Returns (grads, error word); grads is
+    a dict of dx, dg [T, D] (the dtypes of x and g) and dh0 [N, D] fp32 (None
+    unless want_dh0).  Pass ``grads`` (the same dict) to reuse buffers."""
+    c = _Call("gdn_glr_backward", x.device, stream)
+    c.need(x.dim() == 2 and g.dim() == 2, "x, g must be [tokens, channels]")
+    T, D = x.shape
+    ins = _glr_inputs(c, x, g)
+    N, cu = _glr_batch(c, cu_seqlens, n_seqs)
+    dhp, lddh = c.rows(d_h, "d_h", (T, D))
+    if grads is None:
+        grads = {"dx": c.empty((T, D), x.dtype), "dg": c.empty((T, D), g.dtype),
+                 "dh0": c.empty((N, D), torch.float32) if want_dh0 else None}
+    if error is None:
+        error = c.empty((1,), torch.int32)
+    c.need(carry is not None, "carry is the forward's (want_carry=True)")
+    c.run(lib.gdn_glr_backward, *ins, cu, N, T, D, _glr_mode(complement),
+          c.full(carry, "carry", (glr_carry_rows(N, T), D), torch.float32), dhp, lddh,
+          _dtype_code(d_h), c.full(ds_final, "ds_final", (N, D), torch.float32),
+          *c.rows(grads["dx"], "dx", (T, D), x.dtype),
+          *c.rows(grads["dg"], "dg", (T, D), g.dtype),
+          c.full(grads.get("dh0"), "dh0", (N, D), torch.float32),
+          c.full(error, "error", (1,), torch.int32))
+    return grads, error
+
+
+def glr_decode_step(state: GlrDecodeState, x, g, *, slot_idx=None, complement: bool = False,
+                    out_dtype=None, h=None, stream=None):
+    """gdn_glr_decode_step for B rows: x, g [B, D]; row b advances slot slot_idx[b]
+    (int32; slot b without it).  Returns h [B, D]; bad rows set state.error."""
+    c = _Call("gdn_glr_decode_step", x.device, stream)
+    c.need(x.dim() == 2 and g.dim() == 2, "x, g must be [rows, channels]")
+    B, D = x.shape
+    ins = _glr_inputs(c, x, g)
+    odt = _dtype_of(out_dtype, h.dtype if h is not None else x.dtype)
+    if h is None:
+        h = c.empty((B, D), odt)
+    hp, ldh = c.rows(h, "h", (B, D), odt)
+    c.run(lib.gdn_glr_decode_step, *ins, c.full(slot_idx, "slot_idx", (B,), torch.int32), B, D,
+          _glr_mode(complement), _glr_state(c, state, D), hp, ldh, _dtype_code_of(odt))
+    return h
 
 
 def _dt(dtype) -> int:
