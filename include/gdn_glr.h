@@ -28,7 +28,8 @@
  * [tokens, D] may have a row stride (ld*, in elements, >= D) and need only
  * the alignment of their elements; fp32 arrays [rows, D] are contiguous and
  * 16-byte aligned.  g may be -inf (a = 0); it must not be NaN or +inf.
- * D is any size from 1 to 2^24.
+ * D is any size from 1 to 2^24, total_tokens up to 2^31 - 4097, strides up to
+ * 2^27 elements.
  */
 #ifndef GDN_GLR_H
 #define GDN_GLR_H

@@ -55,9 +55,23 @@ def backward(x, g, lengths, d_h, h0=None, ds_final=None, complement=False):
     return dx, dg, u
 
 
-def _aged(a, b, s0, lengths, reverse=False):
+# One step of an fp32 evaluation multiplies every older term by a decay that is
+# off by at most (4 + 1.25 |g|) U (2^x off by 4 U, the rounding of x = g log2 e by
+# |g| U and that of the constant by |g| U / 4; 1 + e of the complement form by less),
+# with one rounding of the running product and one of the running sum:
+# (6 + 1.25 |g|) U.  A term starts with the rounding of its input ((1 - a) x: at
+# most 14 U) and ends with those of the state's last operations: 16 U.  First
+# order; the factor 1.01 covers the products of roundings at these lengths.
+ENDS = 16.0 * 1.01 * U
+
+
+def _step(g):
+    return 1.01 * U * (6.0 + 1.25 * np.minimum(np.abs(np.asarray(g, np.float64)), 200.0))
+
+
+def _aged(a, step, b, s0, lengths, reverse=False):
     """Per element: S = the recurrence over |b| and |s0|, W = the same sum with
-    every term times its age in steps."""
+    every term times what its decays are off by."""
     S, W = np.zeros_like(b), np.zeros_like(b)
     start = 0
     fin_s, fin_w = np.zeros((len(lengths), b.shape[1])), np.zeros((len(lengths), b.shape[1]))
@@ -67,44 +81,37 @@ def _aged(a, b, s0, lengths, reverse=False):
         for t in order:
             if reverse:          # lam = |dh| + mu: kept before the decay
                 s = s + np.abs(b[t])
-                S[t], W[t] = s, w + s
-                s, w = a[t] * s, a[t] * (w + s)
+                S[t], W[t] = s, w
+                s, w = a[t] * s, a[t] * (w + step[t] * s)
             else:
-                s, w = a[t] * s + np.abs(b[t]), a[t] * (w + s)
+                s, w = a[t] * s + np.abs(b[t]), a[t] * (w + step[t] * s)
                 S[t], W[t] = s, w
         fin_s[n], fin_w[n] = s, w
         start += L
     return S, W, fin_s, fin_w
 
 
-# One step of an fp32 evaluation multiplies every older term by a decay that is
-# off by at most 4 U (two units in the last place of expf, or one of expm1f and
-# the rounding of 1 + e), one rounding of the running product and one of the
-# running sum: 6 U.  A term starts with the rounding of its input ((1 - a) x:
-# at most 9 U) and ends with those of the state's last operations: 16 U.  First
-# order; the factor 1.01 covers the products of roundings at these lengths.
-STEP, ENDS = 6.0 * 1.01 * U, 16.0 * 1.01 * U
-
-
 def forward_bound(x, g, lengths, h0=None, complement=False):
     """Elementwise bounds of |h - fp32 h| and |s_final - fp32 s_final|."""
+    step = _step(g)
     x, a, gain = _parts(x, g, complement)
     z = np.zeros((len(lengths), x.shape[1])) if h0 is None else np.asarray(h0, np.float64)
-    S, W, fs, fw = _aged(a, gain * x, z, lengths)
-    return STEP * W + ENDS * S + 1e-36, STEP * fw + ENDS * fs + 1e-36
+    S, W, fs, fw = _aged(a, step, gain * x, z, lengths)
+    return W + ENDS * S + 1e-36, fw + ENDS * fs + 1e-36
 
 
 def backward_bound(x, g, lengths, d_h, h0=None, ds_final=None, complement=False):
     """Elementwise bounds of an fp32 (dx, dg, dh0)."""
     eh, _ = forward_bound(x, g, lengths, h0, complement)
     h, _ = forward(x, g, lengths, h0, complement)
+    step = _step(g)
     x, a, gain = _parts(x, g, complement)
     D = x.shape[1]
     z = np.zeros((len(lengths), D))
-    S, W, fs, fw = _aged(a, np.asarray(d_h, np.float64),
+    S, W, fs, fw = _aged(a, step, np.asarray(d_h, np.float64),
                          z if ds_final is None else np.asarray(ds_final, np.float64), lengths,
                          reverse=True)
-    elam = STEP * W + ENDS * S
+    elam = W + ENDS * S
     edx = np.abs(gain) * (elam + ENDS * S)
     hp, ehp = np.zeros_like(h), np.zeros_like(h)
     start = 0
@@ -114,7 +121,7 @@ def backward_bound(x, g, lengths, d_h, h0=None, ds_final=None, complement=False)
             hp[start + 1:start + L] = h[start:start + L - 1]
             ehp[start + 1:start + L] = eh[start:start + L - 1]
         start += L
-    mu, emu = a * S, a * (elam + ENDS * S)
+    mu, emu = a * S, a * (elam + (ENDS + step) * S)
     size = np.abs(hp) + (np.abs(x) if complement else 0.0)
     edg = emu * (size + ehp) + mu * (ehp + 3 * U * size)
-    return edx + 1e-36, edg + 1e-36, STEP * fw + ENDS * fs + 1e-36
+    return edx + 1e-36, edg + 1e-36, fw + ENDS * fs + 1e-36

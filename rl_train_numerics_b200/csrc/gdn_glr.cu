@@ -1,33 +1,55 @@
 // gdn_glr.cu -- gated linear recurrence with a vector state (gdn_glr.h).
 //
-// h_t = a_t h_{t-1} + b_t per channel, a_t = exp(g_t).  One thread holds V
-// neighbouring channels of one chunk of 16 tokens; a warp holds 32 V channels
-// of a chunk, a block of 8 warps the 8 chunks of a tile of 128 tokens.  For
-// every tile a thread
-//   1. folds its chunk into (A, B) from A = 1, B = 0 (they do not depend on
-//      the state that enters the chunk) and shares them,
-//   2. runs the state over the tile's 8 chunks, H <- fma(A_i, H, B_i), and
-//      keeps the H that enters its own,
-//   3. walks its chunk again and writes h_t = fma(A, H, B).
+// h_t = a_t h_{t-1} + b_t per channel, a_t = exp(g_t).  A block takes a slab of
+// 32 channels of one sequence and walks it in tiles of 128 tokens, 8 chunks of
+// 16; one thread holds V neighbouring channels of one chunk.  For every tile
+//   1. a thread folds its chunk into the maps (A_t, B_t) from A = 1, B = 0,
+//      which do not depend on the state that enters the chunk, and shares the
+//      last of them;
+//   2. one warp runs the state over the chunks, H <- fma(A, H, B), a lane per
+//      channel;
+//   3. a thread writes h_t = fma(A_t, H, B_t) of its chunk.
 // The last h of a chunk is the next chunk's H by the same operations, so the
 // decode step, which keeps (H, A, B), has the forward's bits.  Every channel's
 // operations are those of its own sequence in order, so nothing depends on
-// the batch, on V or on how tiles are spread over blocks.
+// the batch, on V or on how tiles are spread over blocks.  Tokens behind a
+// sequence's end are identity steps (a = 1, b = 0), which leave A, B and H as
+// they are.
 //
-// Tokens behind a sequence's end are identity steps (a = 1, b = 0), which
-// leave A, B and H as they are, bit for bit.
+// Few sequences of few channels would leave most of the device idle: then a
+// cluster of 2, 4 or 8 blocks takes as many neighbouring tiles at a time, every
+// block writes its chunks' maps into all blocks' shared memory, and each runs
+// the state over all of them.  The data are still read once.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
 #include "../../include/gdn_glr.h"
 #include "gdn_common.cuh"
+#include "gdn_mma.cuh"
+#include "gdn_tmap.h"
+#include "gdn_umma.cuh"
 
 namespace gdn {
 
+namespace cg = cooperative_groups;
+
 constexpr int kGlrChunk = GDN_GLR_CHUNK;
-constexpr int kGlrWarps = 8;
-constexpr int kGlrThreads = 32 * kGlrWarps;
-constexpr int kGlrTile = kGlrChunk * kGlrWarps;
+constexpr int kGlrChunks = 8;   // chunks of a tile
+constexpr int kGlrTile = kGlrChunk * kGlrChunks;
+constexpr int kGlrSlab = 32;    // channels of a block
+constexpr int kGlrMaxCluster = 8;
+constexpr int kGlrMaxStages = 8;
+constexpr int kGlrPolls = 1 << 22;
+// Blocks of a multiprocessor that a kernel's registers leave room for.
+template <int V>
+__host__ __device__ constexpr int glr_blocks(bool forward) {
+  return V == 1 ? 2 : forward ? 4 : 3;
+}
+template <int V>
+constexpr int kGlrThreads = kGlrChunks * kGlrSlab / V;  // that compute
+template <int V>
+constexpr int kGlrBlock = kGlrThreads<V> + 32;  // and the service warp
 static_assert(kGlrTile == GDN_GLR_TILE, "carry rows are tile starts");
 
 // V consecutive elements as loaded, all-zero bits for masked ones.
@@ -81,63 +103,103 @@ __device__ __forceinline__ typename Raw<T, V>::type raw_load(const T* p) {
   return *reinterpret_cast<const typename Raw<T, V>::type*>(p);
 }
 
+// a = exp(g) as 2^(g log2 e), by ex2.approx (relative error at most 2^-22 = 4 U,
+// U = 2^-24).  The rounded product adds |g| U and the rounded constant |g| U / 4
+// to it, relative to a: a weight of e^-G carries an error of at most 1.25 G U
+// e^-G < U / 2 of what it weighs, so the states are as good as with an exact
+// exponential, for 2 instructions.  -inf gives 0, a NaN stays one.
+__device__ __forceinline__ float decay(float g) {
+  float a;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(__fmul_rn(g, 1.4426950408889634f)));
+  return a;
+}
+// exp(g) - 1 for |g| <= 1/2: the Taylor series to g^8 / 8! (the rest is below
+// 2^-26 of it).
+__device__ __forceinline__ float decay_m1(float g) {
+  float s = 1.f / 40320.f;
+  s = __fmaf_rn(s, g, 1.f / 5040.f);
+  s = __fmaf_rn(s, g, 1.f / 720.f);
+  s = __fmaf_rn(s, g, 1.f / 120.f);
+  s = __fmaf_rn(s, g, 1.f / 24.f);
+  s = __fmaf_rn(s, g, 1.f / 6.f);
+  s = __fmaf_rn(s, g, 0.5f);
+  s = __fmaf_rn(s, g, 1.f);
+  return __fmul_rn(s, g);
+}
+
 // The gate of one token: a thread keeps one float `w` of it, from which the
 // decay a and the input b come.  PLAIN: w = a.  COMPLEMENT needs a and 1 - a,
-// each with its own relative accuracy: a decay below exp(-1/2) is kept as a
-// (1 - a loses nothing there), the others as e = expm1(g), with a = 1 + e and
-// 1 - a = -e; bit `i` of `low` says which.
+// each with its own relative accuracy: for |g| < 1/2 it keeps e = exp(g) - 1,
+// with a = 1 + e and 1 - a = -e, for the others a (1 - a loses little there);
+// bit `i` of `far` says which.
 template <int MODE>
-__device__ __forceinline__ float gate_of(float g, unsigned& low, int i) {
-  if (MODE == GDN_GLR_INPUT_PLAIN) return expf(g);
-  const bool decayed = g < -0.5f;
-  low |= (unsigned)decayed << i;
-  return decayed ? expf(g) : expm1f(g);
+__device__ __forceinline__ float gate_of(float g, unsigned& far, int i) {
+  if (MODE == GDN_GLR_INPUT_PLAIN) return decay(g);
+  const bool is_far = !(fabsf(g) < 0.5f);
+  far |= (unsigned)is_far << i;
+  const float a = decay(g), e = decay_m1(g);  // both: a branch for each token costs far more
+  return is_far ? a : e;
 }
 template <int MODE>
-__device__ __forceinline__ float gate_a(float w, unsigned low, int i) {
+__device__ __forceinline__ float gate_a(float w, unsigned far, int i) {
   if (MODE == GDN_GLR_INPUT_PLAIN) return w;
-  return low >> i & 1 ? w : __fadd_rn(1.f, w);
+  return far >> i & 1 ? w : __fadd_rn(1.f, w);
 }
 template <int MODE>
-__device__ __forceinline__ float gate_b(float w, unsigned low, int i, float x) {
+__device__ __forceinline__ float gate_b(float w, unsigned far, int i, float x) {
   if (MODE == GDN_GLR_INPUT_PLAIN) return x;
-  return __fmul_rn(low >> i & 1 ? __fsub_rn(1.f, w) : -w, x);
+  return __fmul_rn(far >> i & 1 ? __fsub_rn(1.f, w) : -w, x);
 }
 
 struct GlrArgs {
   const void* x;
   const void* g;
-  int64_t ldx, ldg;
+  int ldx, ldg;
   const int32_t* cu;
   int N;
-  int64_t T;
-  int D, slabs;
+  int T, D, slabs, stages;
   const float* h0;  // forward
   void* h;
-  int64_t ldh;
+  int ldh;
   float* s_final;
   gdn_glr_state st;  // st.h == nullptr: none
   const int32_t* slot_idx;
   float* carry;
   const void* d_h;  // backward
-  int64_t lddh;
+  int lddh;
   const float* ds_final;
   void* d_x;
-  int64_t lddx;
+  int lddx;
   void* d_g;
-  int64_t lddg;
+  int lddg;
   float* d_h0;
   int32_t* error;
 };
 
-__device__ __forceinline__ bool glr_seq_ok(const GlrArgs& p, int n) {
-  return p.cu[0] == 0 && (int64_t)p.cu[p.N] == p.T && p.cu[n] >= 0 && p.cu[n + 1] >= p.cu[n] &&
-         (int64_t)p.cu[n + 1] <= p.T;
+// Tensor maps of the staged kernels' inputs.
+struct GlrBoxes {
+  CUtensorMap x, g, dh;
+};
+
+// First token and length of sequence n; false when cu_seqlens does not start at
+// 0, end at T and ascend here.  The four loads are independent of each other.
+__device__ __forceinline__ bool glr_seq(const GlrArgs& p, int n, int& start, int& length) {
+  const int zero = p.cu[0], total = p.cu[p.N], first = p.cu[n], end = p.cu[n + 1];
+  start = first;
+  length = end - first;
+  return (zero == 0) & (total == p.T) & (first >= 0) & (end >= first) & (end <= p.T);
 }
 
-// Slot of row n, or -1 when it is out of range or an earlier row has it too
-// (the whole block calls this; every thread gets the answer).
+// Slot of row n, or -1 when it is out of range or an earlier row has it too.
+// Any threads call the first form, the whole block the second.
 __device__ __forceinline__ int glr_slot(const int32_t* slot_idx, int n, int n_slots) {
+  if (!slot_idx) return n < n_slots ? n : -1;
+  const int slot = slot_idx[n];
+  bool twice = false;
+  for (int i = 0; i < n; i++) twice |= slot_idx[i] == slot;
+  return slot >= 0 && slot < n_slots && !twice ? slot : -1;
+}
+__device__ __forceinline__ int glr_slot_block(const int32_t* slot_idx, int n, int n_slots) {
   if (!slot_idx) return n < n_slots ? n : -1;
   const int slot = slot_idx[n];
   int twice = 0;
@@ -146,270 +208,630 @@ __device__ __forceinline__ int glr_slot(const int32_t* slot_idx, int n, int n_sl
   return slot >= 0 && slot < n_slots && !twice ? slot : -1;
 }
 
+// Channels ch .. ch + V - 1 of a row of an fp32 [rows, D] array; zeros without
+// one and from D on.
 template <int V>
-__device__ __forceinline__ void row_get(const float* base, int64_t row, int D, int ch, bool live,
+__device__ __forceinline__ void row_get(const float* base, int64_t row, int D, int ch,
                                         float (&f)[V]) {
 #pragma unroll
-  for (int v = 0; v < V; v++) f[v] = 0.f;
-  if (base && live) {
-#pragma unroll
-    for (int v = 0; v < V; v++) f[v] = base[row * D + ch + v];
+  for (int v = 0; v < V; v++) f[v] = base && ch + v < D ? base[row * D + ch + v] : 0.f;
+}
+
+// The first block checks every entry of cu_seqlens and is the only one that
+// clears the error word, so no launch is needed for it.
+__device__ __forceinline__ void glr_report(const GlrArgs& p) {
+  if (blockIdx.x != 0 || !p.error) return;
+  int bad = p.cu[0] != 0 || p.cu[p.N] != p.T;
+  for (int i = threadIdx.x; i < p.N; i += blockDim.x) bad |= p.cu[i + 1] < p.cu[i];
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *p.error = bad ? kErrCuSeqlens : 0;
+}
+
+// Where a thread stands: its block takes tile rank, rank + cs, ... of slab
+// `slab` of sequence n; the thread channels ch .. ch + V - 1 of chunk c.
+struct GlrPlace {
+  int n, slab, rank, cs, c, col, ch;
+  bool live;
+  int L, start, steps, tiles;  // steps of cs tiles; the block's own tiles
+};
+
+template <int V>
+__device__ __forceinline__ bool glr_place(const GlrArgs& p, GlrPlace& at) {
+  at.cs = (int)cg::this_cluster().num_blocks();
+  at.rank = (int)cg::this_cluster().block_rank();
+  const int unit = blockIdx.x / at.cs;
+  at.n = unit / p.slabs;
+  at.slab = unit % p.slabs;
+  glr_report(p);
+  if (!glr_seq(p, at.n, at.start, at.L)) return false;  // the same for a whole cluster
+  at.c = threadIdx.x / (kGlrSlab / V);
+  at.col = threadIdx.x % (kGlrSlab / V) * V;
+  at.ch = at.slab * kGlrSlab + at.col;
+  at.live = at.ch < p.D;
+  const int tiles = at.L / kGlrTile + (at.L % kGlrTile != 0);
+  at.steps = (tiles + at.cs - 1) / at.cs;
+  at.tiles = (tiles + at.cs - 1 - at.rank) / at.cs;
+  return true;
+}
+
+// Tokens of the chunk at t0 that exist.
+__device__ __forceinline__ int chunk_tokens(const GlrPlace& at, int t0) {
+  return min(kGlrChunk, max(0, at.L - t0));
+}
+
+// Row t of a chunk: one 32 x 32-bit product (strides are at most 2^27).
+template <class T>
+__device__ __forceinline__ T* row_at(T* row, int ld, int t) {
+  return row + (int64_t)ld * t;
+}
+
+// The maps of one step's chunks, [cs * 8][32] pairs (multiplier, summand), from
+// every block of the cluster.  The threads of a lone block store them and meet
+// a block barrier.  Blocks of a cluster send them with st.async, whose bytes
+// count on the receiver's mbarrier: a cluster barrier would have to wait for
+// the h that each block has just written to global memory, too.
+//
+// Two maps are used in turn.  A thread sends step s + 2 behind its wait for
+// s + 1, which needs what every thread of every block sends for s + 1, and
+// that it sends behind its own reads of step s; so a map is not overwritten
+// while it is read, and its barrier is in the right phase.
+struct GlrMaps {
+  float2* base;    // [2][cs * 8][32]
+  uint64_t* full;  // [2]
+  int cs;
+  bool late;
+  __device__ __forceinline__ void init(void* mem, uint64_t* bars, int blocks) {
+    base = static_cast<float2*>(mem);
+    full = bars;
+    cs = blocks;
+    late = false;
+    if (cs == 1) return;
+    if (threadIdx.x == 0) {
+      mbar_init(smem_u32(&full[0]), 1);
+      mbar_init(smem_u32(&full[1]), 1);
+      fence_mbar_init();
+    }
+    cg::this_cluster().sync();  // every block has started and has its barriers
+  }
+  __device__ __forceinline__ float2* at(int s) const {
+    return base + (s & 1) * cs * kGlrChunks * kGlrSlab;
+  }
+  // Bytes this block will receive for step s.
+  __device__ __forceinline__ void expect(int s) {
+    if (cs > 1 && threadIdx.x == 0)
+      mbar_expect_tx(smem_u32(&full[s & 1]),
+                     (uint32_t)(cs * kGlrChunks * kGlrSlab * sizeof(float2)));
+  }
+  // The maps of the other blocks (the block's own are there behind its barrier).
+  __device__ __forceinline__ void wait(int s) {
+    if (cs == 1) return;
+    const uint32_t bar = smem_u32(&full[s & 1]), parity = (uint32_t)(s >> 1 & 1);
+    for (int i = late ? kGlrPolls - (1 << 12) : 0; i < kGlrPolls; i++) {
+      uint32_t done;  // acquires what other blocks sent
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}\n"
+          : "=r"(done)
+          : "r"(bar), "r"(parity)
+          : "memory");
+      if (done) return;
+    }
+    late = true;
+  }
+};
+
+__device__ __forceinline__ uint32_t remote(uint32_t addr, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void send(uint32_t dst, uint32_t mbar, float x, float y) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::
+          "r"(dst),
+      "r"(__float_as_uint(x)), "r"(__float_as_uint(y)), "r"(mbar)
+      : "memory");
+}
+__device__ __forceinline__ void send(uint32_t dst, uint32_t mbar, float x, float y, float z,
+                                     float w) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, "
+      "[%5];" ::"r"(dst),
+      "r"(__float_as_uint(x)), "r"(__float_as_uint(y)), "r"(__float_as_uint(z)),
+      "r"(__float_as_uint(w)), "r"(mbar)
+      : "memory");
+}
+
+// Share (a, b) of this thread's chunk with every block of the cluster.
+template <int V>
+__device__ __forceinline__ void glr_share(const GlrMaps& m, int s, const GlrPlace& at,
+                                          const float (&a)[V], const float (&b)[V]) {
+  float2* to = m.at(s) + (at.rank * kGlrChunks + at.c) * kGlrSlab + at.col;
+  if (m.cs == 1) {
+    if (V == 1)
+      *to = make_float2(a[0], b[0]);
+    else
+      *reinterpret_cast<float4*>(to) = make_float4(a[0], b[0], a[V - 1], b[V - 1]);
+    return;
+  }
+  const uint32_t dst = smem_u32(to), bar = smem_u32(&m.full[s & 1]);
+  for (int r = 0; r < m.cs; r++) {
+    if (V == 1)
+      send(remote(dst, r), remote(bar, r), a[0], b[0]);
+    else
+      send(remote(dst, r), remote(bar, r), a[0], b[0], a[V - 1], b[V - 1]);
   }
 }
 
-// One block per (sequence, slab of 32 V channels).
-template <class IN, class G, class OUT, int V, int MODE>
-__global__ void __launch_bounds__(kGlrThreads) k_glr_forward(const GlrArgs p) {
-  __shared__ float sA[2][kGlrWarps][32 * V], sB[2][kGlrWarps][32 * V];
-  const int n = blockIdx.x / p.slabs, slab = blockIdx.x % p.slabs;
-  if (!glr_seq_ok(p, n)) {
-    if (threadIdx.x == 0 && p.error) atomicOr(p.error, kErrCuSeqlens);
+// Run the service warp's channel z over the maps of 8 chunks (REVERSE: last
+// first) and, where they are the block's own, keep what enters each of them.
+// All are loaded before the chain, so that its steps are dependent products
+// alone.
+template <bool REVERSE>
+__device__ __forceinline__ float glr_chain(const float2* maps, float z, int lane, bool own,
+                                           float (&enter)[kGlrChunks][kGlrSlab]) {
+  float2 m[kGlrChunks];
+#pragma unroll
+  for (int i = 0; i < kGlrChunks; i++) m[i] = maps[i * kGlrSlab + lane];
+#pragma unroll
+  for (int k = 0; k < kGlrChunks; k++) {
+    const int i = REVERSE ? kGlrChunks - 1 - k : k;
+    if (own) enter[i][lane] = z;
+    z = __fmaf_rn(m[i].x, z, m[i].y);
+  }
+  return z;
+}
+
+// How a thread gets V neighbouring elements of its chunk's tokens.
+//
+// Staged: the block's tile (128 tokens x 32 channels) is copied by one tensor
+// map box into shared memory, two steps ahead; a thread reads its own slots.
+// Rows behind the sequence's end hold the next sequence's tokens and are
+// cleared by the threads that own them.
+//
+// Direct (rows that a tensor map cannot describe: a base or stride off 16
+// bytes, an odd width): loads from global memory, all of the chunk's at once.
+template <class T, int V, bool STAGED>
+struct GlrSource;
+
+template <class T, int V>
+struct GlrSource<T, V, true> {
+  using R = typename Raw<T, V>::type;
+  T* tile;  // this thread's column of its chunk's first token in the stage
+  __device__ __forceinline__ void set(T* stage, const GlrPlace& at) {
+    tile = stage + at.c * kGlrChunk * kGlrSlab + at.col;
+  }
+  __device__ __forceinline__ R get(int t) const { return raw_load<T, V>(tile + t * kGlrSlab); }
+  __device__ __forceinline__ void clear_from(int have) {
+    R zero;
+    raw_zero(zero);
+    for (int t = have; t < kGlrChunk; t++) *reinterpret_cast<R*>(tile + t * kGlrSlab) = zero;
+  }
+};
+
+template <class T, int V>
+struct GlrSource<T, V, false> {
+  using R = typename Raw<T, V>::type;
+  R r[kGlrChunk];
+  __device__ __forceinline__ void load(const T* row, int ld, int have) {
+    if (have == kGlrChunk) {
+#pragma unroll
+      for (int t = 0; t < kGlrChunk; t++) r[t] = raw_load<T, V>(row_at(row, ld, t));
+    } else {
+#pragma unroll
+      for (int t = 0; t < kGlrChunk; t++) {
+        raw_zero(r[t]);
+        if (t < have) r[t] = raw_load<T, V>(row_at(row, ld, t));
+      }
+    }
+  }
+  __device__ __forceinline__ R get(int t) const { return r[t]; }
+};
+
+__device__ __forceinline__ void glr_prefetch(const GlrBoxes& box) {
+  for (const CUtensorMap* m : {&box.g, &box.x, &box.dh})
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+// 2-D tensor-map load of one box into shared memory (x * the element size is
+// a multiple of 16 bytes: slabs are 32 channels).
+__device__ __forceinline__ void glr_box(void* dst, const CUtensorMap* map, int x, int y,
+                                        uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar)
+      : "memory");
+}
+
+// The next place in a ring of stages, and the parity of its wait.
+struct GlrRing {
+  int n, slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ explicit GlrRing(int stages) : n(stages) {}
+  __device__ __forceinline__ void next() {
+    if (++slot == n) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// The ring's barriers, which count the copies' bytes, and the place of the
+// next tile to take.  A wait gives up after kGlrPolls polls, and then the
+// kernel goes on without waiting (every block still meets every barrier) and
+// reports.
+struct GlrPipe : GlrRing {
+  uint64_t* full;  // [kGlrMaxStages]
+  bool late = false;
+  using GlrRing::GlrRing;
+  __device__ __forceinline__ void init(uint64_t* bars) {
+    full = bars;
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < n; i++) mbar_init(smem_u32(&full[i]), 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void wait() {
+    if (!mbar_wait(smem_u32(&full[slot]), parity, late ? 1 << 12 : kGlrPolls)) late = true;
+  }
+};
+
+template <class IN, class G>
+struct GlrForwardStage {
+  alignas(128) G g[kGlrTile * kGlrSlab];
+  alignas(128) IN x[kGlrTile * kGlrSlab];
+};
+
+__device__ __forceinline__ unsigned char* align128(unsigned char* p) {
+  return p + ((128u - (smem_u32(p) & 127u)) & 127u);
+}
+
+template <class IN, class G, class OUT, int V, int MODE, bool STAGED>
+__global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(true))
+    k_glr_forward(const GlrArgs p, const __grid_constant__ GlrBoxes box) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(16) float enter[kGlrChunks][kGlrSlab];
+  __shared__ uint64_t bars[2 + kGlrMaxStages];
+  using Stage = GlrForwardStage<IN, G>;
+  unsigned char* smem = align128(smem_raw);
+  Stage* stage = reinterpret_cast<Stage*>(smem);
+  GlrPlace at;
+  if (STAGED && threadIdx.x == 0) glr_prefetch(box);
+  if (!glr_place<V>(p, at)) return;
+  const int step_tokens = at.cs * kGlrTile;
+  GlrMaps maps;
+  maps.init(smem + (STAGED ? p.stages * sizeof(Stage) : 0), bars, at.cs);
+  GlrPipe pipe(p.stages);
+  if (STAGED) pipe.init(bars + 2);
+  if (threadIdx.x >= kGlrThreads<V>) {
+    // The service warp copies the block's tiles in order into the ring of stages
+    // and runs the state over the chunks.
+    const int lane = threadIdx.x & 31, ch = at.slab * kGlrSlab + lane;
+    int copied = 0;
+    auto issue = [&]() {
+      if (!STAGED || copied >= at.tiles) return;
+      if (lane == 0) {
+        Stage& d = stage[pipe.slot];
+        const int row = at.start + copied * step_tokens + at.rank * kGlrTile;
+        const uint32_t bar = smem_u32(&pipe.full[pipe.slot]);
+        mbar_expect_tx(bar, kGlrTile * kGlrSlab * (uint32_t)(sizeof(IN) + sizeof(G)));
+        glr_box(d.g, &box.g, at.slab * kGlrSlab, row, bar);
+        glr_box(d.x, &box.x, at.slab * kGlrSlab, row, bar);
+      }
+      copied++;
+      pipe.next();
+    };
+    for (int j = 0; j < p.stages; j++) issue();
+    float H[1];
+    row_get<1>(p.h0, at.n, p.D, ch, H);
+    for (int s = 0; s < at.steps; s++) {
+      __syncthreads();  // every warp has folded its chunks of the step
+      maps.wait(s);
+      for (int r = 0; r < at.cs; r++)
+        H[0] = glr_chain<false>(maps.at(s) + r * kGlrChunks * kGlrSlab, H[0], lane, r == at.rank,
+                                enter);
+      __syncthreads();
+      issue();
+      if (p.carry && s < at.tiles && ch < p.D)
+        p.carry[(int64_t)(at.start / kGlrTile + at.n + s * at.cs + at.rank) * p.D + ch] =
+            enter[0][lane];
+    }
+    if (maps.late && p.error) atomicOr(p.error, kErrTimeout);
+    __syncwarp();
+    if (at.cs > 1) cg::this_cluster().sync();
     return;
   }
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int ch = (slab * 32 + lane) * V;
-  const bool live = ch < p.D;
-  const int64_t L = (int64_t)p.cu[n + 1] - p.cu[n];
-  const IN* x = static_cast<const IN*>(p.x) + (int64_t)p.cu[n] * p.ldx + ch;
-  const G* g = static_cast<const G*>(p.g) + (int64_t)p.cu[n] * p.ldg + ch;
-  OUT* h = static_cast<OUT*>(p.h) + (int64_t)p.cu[n] * p.ldh + ch;
-  float* carry = p.carry ? p.carry + ((int64_t)p.cu[n] / kGlrTile + n) * p.D + ch : nullptr;
-
-  float H[V], Hm[V], A[V], B[V], hv[V];
-  row_get<V>(p.h0, n, p.D, ch, live, H);
+  float Hm[V], hv[V], A[kGlrChunk][V], B[kGlrChunk][V];
+  row_get<V>(p.h0, at.n, p.D, at.ch, hv);
 #pragma unroll
   for (int v = 0; v < V; v++) {
-    Hm[v] = hv[v] = H[v];
-    A[v] = 1.f;
-    B[v] = 0.f;
+    Hm[v] = hv[v];
+    A[kGlrChunk - 1][v] = 1.f;
+    B[kGlrChunk - 1][v] = 0.f;
   }
-  const int64_t ntiles = (L + kGlrTile - 1) / kGlrTile;
-  for (int64_t s = 0; s < ntiles; s++) {
-    const int64_t t0 = s * kGlrTile + w * kGlrChunk;
-    typename Raw<IN, V>::type rx[kGlrChunk];
-    float ga[kGlrChunk][V];
-    unsigned low = 0;
-#pragma unroll
-    for (int t = 0; t < kGlrChunk; t++) {
-      typename Raw<G, V>::type rg;
-      raw_zero(rx[t]);
-      raw_zero(rg);
-      if (live && t0 + t < L) {
-        rx[t] = raw_load<IN, V>(x + (t0 + t) * p.ldx);
-        rg = raw_load<G, V>(g + (t0 + t) * p.ldg);
+  const IN* x = static_cast<const IN*>(p.x) + (int64_t)at.start * p.ldx + at.ch;
+  const G* g = static_cast<const G*>(p.g) + (int64_t)at.start * p.ldg + at.ch;
+  OUT* h = static_cast<OUT*>(p.h) + (int64_t)at.start * p.ldh + at.ch;
+  int t0 = at.rank * kGlrTile + at.c * kGlrChunk;
+  for (int s = 0; s < at.steps; s++, t0 += step_tokens) {
+    const int tokens = chunk_tokens(at, t0), have = at.live ? tokens : 0;
+    GlrSource<IN, V, STAGED> sx;
+    GlrSource<G, V, STAGED> sg;
+    if (s < at.tiles) {
+      if constexpr (STAGED) {
+        sx.set(stage[pipe.slot].x, at);
+        sg.set(stage[pipe.slot].g, at);
+        pipe.wait();
+        if (tokens < kGlrChunk) {
+          sx.clear_from(tokens);
+          sg.clear_from(tokens);
+        }
+      } else {
+        sx.load(x + (int64_t)t0 * p.ldx, p.ldx, have);
+        sg.load(g + (int64_t)t0 * p.ldg, p.ldg, have);
       }
-      widen(rg, ga[t]);
-    }
 #pragma unroll
-    for (int v = 0; v < V; v++) {
-      A[v] = 1.f;
-      B[v] = 0.f;
-    }
+      for (int t = 0; t < kGlrChunk; t++) {
+        float xv[V], gv[V];
+        widen(sx.get(t), xv);
+        widen(sg.get(t), gv);
 #pragma unroll
-    for (int t = 0; t < kGlrChunk; t++) {
-      float xv[V];
-      widen(rx[t], xv);
+        for (int v = 0; v < V; v++) {
+          unsigned far = 0;
+          const float k = gate_of<MODE>(gv[v], far, 0), a = gate_a<MODE>(k, far, 0);
+          const float b = gate_b<MODE>(k, far, 0, xv[v]);
+          A[t][v] = t ? __fmul_rn(a, A[t - 1][v]) : a;
+          B[t][v] = t ? __fmaf_rn(a, B[t - 1][v], b) : __fmaf_rn(a, 0.f, b);
+        }
+      }
+    } else {  // only in a cluster's last step: this block's tile is behind the end
 #pragma unroll
       for (int v = 0; v < V; v++) {
-        ga[t][v] = gate_of<MODE>(ga[t][v], low, t * V + v);
-        const float a = gate_a<MODE>(ga[t][v], low, t * V + v);
-        A[v] = __fmul_rn(a, A[v]);
-        B[v] = __fmaf_rn(a, B[v], gate_b<MODE>(ga[t][v], low, t * V + v, xv[v]));
+        A[kGlrChunk - 1][v] = 1.f;
+        B[kGlrChunk - 1][v] = 0.f;
       }
     }
-    // Two buffers: a thread writes one again only behind the other's barrier,
-    // which every thread reaches after its reads of the first.
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-      sA[s & 1][w][lane * V + v] = A[v];
-      sB[s & 1][w][lane * V + v] = B[v];
-    }
+    maps.expect(s);
+    glr_share<V>(maps, s, at, A[kGlrChunk - 1], B[kGlrChunk - 1]);
     __syncthreads();
+    if (STAGED) pipe.next();
+    __syncthreads();  // the service warp has handed over
+    if (have == 0) continue;
 #pragma unroll
-    for (int i = 0; i < kGlrWarps; i++)
+    for (int v = 0; v < V; v++) Hm[v] = enter[at.c][at.col + v];
+    OUT* out = h + (int64_t)t0 * p.ldh;
+    if (have == kGlrChunk) {
 #pragma unroll
-      for (int v = 0; v < V; v++) {
-        if (i == w) Hm[v] = H[v];
-        H[v] = __fmaf_rn(sA[s & 1][i][lane * V + v], H[v], sB[s & 1][i][lane * V + v]);
+      for (int t = 0; t < kGlrChunk; t++) {
+#pragma unroll
+        for (int v = 0; v < V; v++) hv[v] = __fmaf_rn(A[t][v], Hm[v], B[t][v]);
+        put(row_at(out, p.ldh, t), hv);
       }
-    if (carry && live && w == 0) put(carry + s * p.D, Hm);
-    if (!live || t0 >= L) continue;
+    } else {
 #pragma unroll
-    for (int v = 0; v < V; v++) {
-      A[v] = 1.f;
-      B[v] = 0.f;
-    }
+      for (int t = 0; t < kGlrChunk; t++) {
 #pragma unroll
-    for (int t = 0; t < kGlrChunk; t++) {
-      float xv[V];
-      widen(rx[t], xv);
-#pragma unroll
-      for (int v = 0; v < V; v++) {
-        const float a = gate_a<MODE>(ga[t][v], low, t * V + v);
-        A[v] = __fmul_rn(a, A[v]);
-        B[v] = __fmaf_rn(a, B[v], gate_b<MODE>(ga[t][v], low, t * V + v, xv[v]));
-        hv[v] = __fmaf_rn(A[v], Hm[v], B[v]);
+        for (int v = 0; v < V; v++) hv[v] = __fmaf_rn(A[t][v], Hm[v], B[t][v]);
+        if (t < have) put(row_at(out, p.ldh, t), hv);
       }
-      if (t0 + t < L) put(h + (t0 + t) * p.ldh, hv);
     }
   }
-  // The warp that holds the last token has its h and the chunk's (Hm, A, B).
-  const int last_w = L > 0 ? (int)((L - 1) / kGlrChunk % kGlrWarps) : 0;
-  if (p.s_final && live && w == last_w) put(p.s_final + (int64_t)n * p.D + ch, hv);
+  if (pipe.late && p.error) atomicOr(p.error, kErrTimeout);
+  if (at.cs > 1) {  // nothing is on its way to a block that ends
+    __syncwarp();
+    cg::this_cluster().sync();
+  }
+  // The thread that holds the last token has its h and the chunk's (Hm, A, B):
+  // the identity steps behind the last token have left them.
+  const int tail = at.L > 0 ? (at.L - 1) / kGlrChunk % (at.cs * kGlrChunks) : 0;
+  const bool mine = at.live && at.rank * kGlrChunks + at.c == tail;
+  if (p.s_final && mine) put(p.s_final + (int64_t)at.n * p.D + at.ch, hv);
   if (p.st.h) {
-    const int slot = glr_slot(p.slot_idx, n, p.st.n_slots);
-    const int pos = (int)(L % kGlrChunk);
+    if (!mine && !(at.slab == 0 && at.rank == 0 && threadIdx.x == 0)) return;
+    const int slot = glr_slot(p.slot_idx, at.n, p.st.n_slots);
+    const int pos = (int)(at.L % kGlrChunk);
     if (slot < 0) {
-      if (threadIdx.x == 0) atomicOr(p.st.error, kErrPos);
+      atomicOr(p.st.error, kErrPos);
       return;
     }
-    if (slab == 0 && threadIdx.x == 0) p.st.pos[slot] = pos;
-    if (live && w == last_w) {
-      const float one[2] = {1.f, 1.f}, zero[2] = {0.f, 0.f};
-      const int64_t at = (int64_t)slot * p.D + ch;
+    if (at.slab == 0 && at.rank == 0 && threadIdx.x == 0) p.st.pos[slot] = pos;
+    if (mine) {
+      const int64_t to = (int64_t)slot * p.D + at.ch;
 #pragma unroll
       for (int v = 0; v < V; v++) {
-        p.st.h[at + v] = pos ? Hm[v] : hv[v];
-        p.st.a[at + v] = pos ? A[v] : one[v];
-        p.st.b[at + v] = pos ? B[v] : zero[v];
+        p.st.h[to + v] = pos ? Hm[v] : hv[v];
+        p.st.a[to + v] = pos ? A[kGlrChunk - 1][v] : 1.f;
+        p.st.b[to + v] = pos ? B[kGlrChunk - 1][v] : 0.f;
       }
     }
   }
 }
 
-// Reverse mode: tiles from a sequence's last to its first.  A chunk's map of
-// the adjoint mu is mu -> fma(A, mu, M) with the A of the forward and M its
-// value from mu = 0, so the chunks of a tile are again evaluated side by
+// Reverse mode: steps from a sequence's last to its first.  A chunk's map of
+// the adjoint mu is mu -> fma(A, mu, M) with the A of the forward and
+// M = sum A_t dh_t over the chunk, so the chunks of a step are again evaluated side by
 // side; h_{t-1} comes from the tile's carry row and the chunks' (A, B) by the
 // forward's operations.
-template <class IN, class G, class OUT, int V, int MODE>
-__global__ void __launch_bounds__(kGlrThreads) k_glr_backward(const GlrArgs p) {
-  __shared__ float sA[2][kGlrWarps][32 * V], sB[2][kGlrWarps][32 * V], sM[2][kGlrWarps][32 * V];
-  const int n = blockIdx.x / p.slabs, slab = blockIdx.x % p.slabs;
-  if (!glr_seq_ok(p, n)) {
-    if (threadIdx.x == 0 && p.error) atomicOr(p.error, kErrCuSeqlens);
+template <class IN, class G, class OUT>
+struct GlrBackwardStage {
+  alignas(128) G g[kGlrTile * kGlrSlab];
+  alignas(128) IN x[kGlrTile * kGlrSlab];
+  alignas(128) OUT dh[kGlrTile * kGlrSlab];
+};
+
+template <class IN, class G, class OUT, int V, int MODE, bool STAGED>
+__global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(false))
+    k_glr_backward(const GlrArgs p, const __grid_constant__ GlrBoxes box) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(16) float enter[kGlrChunks][kGlrSlab];
+  __shared__ __align__(16) float enter_mu[kGlrChunks][kGlrSlab];
+  __shared__ __align__(16) float2 own[kGlrChunks][kGlrSlab];  // (A, B) of the block's chunks
+  __shared__ uint64_t bars[2 + kGlrMaxStages];
+  using Stage = GlrBackwardStage<IN, G, OUT>;
+  unsigned char* smem = align128(smem_raw);
+  Stage* stage = reinterpret_cast<Stage*>(smem);
+  GlrPlace at;
+  if (STAGED && threadIdx.x == 0) glr_prefetch(box);
+  if (!glr_place<V>(p, at)) return;
+  const int step_tokens = at.cs * kGlrTile;
+  GlrMaps maps;
+  maps.init(smem + (STAGED ? p.stages * sizeof(Stage) : 0), bars, at.cs);
+  GlrPipe pipe(p.stages);
+  // A block without a tile in the last step starts one step later than the others.
+  const int skip = at.steps - at.tiles;
+  if (STAGED) pipe.init(bars + 2);
+  if (threadIdx.x >= kGlrThreads<V>) {
+    // The service warp copies the block's tiles, last first, and runs mu over the
+    // cluster's chunks and the state over the block's own.
+    const int lane = threadIdx.x & 31, ch = at.slab * kGlrSlab + lane;
+    int left = at.tiles;
+    auto issue = [&]() {
+      if (!STAGED || left <= 0) return;
+      left--;
+      if (lane == 0) {
+        Stage& d = stage[pipe.slot];
+        const int row = at.start + left * step_tokens + at.rank * kGlrTile;
+        const uint32_t bar = smem_u32(&pipe.full[pipe.slot]);
+        mbar_expect_tx(bar,
+                       kGlrTile * kGlrSlab * (uint32_t)(sizeof(IN) + sizeof(G) + sizeof(OUT)));
+        glr_box(d.g, &box.g, at.slab * kGlrSlab, row, bar);
+        glr_box(d.x, &box.x, at.slab * kGlrSlab, row, bar);
+        glr_box(d.dh, &box.dh, at.slab * kGlrSlab, row, bar);
+      }
+      pipe.next();
+    };
+    for (int j = 0; j < p.stages; j++) issue();
+    const float* carry = p.carry + (int64_t)(at.start / kGlrTile + at.n) * p.D;
+    auto entering = [&](int i) {  // the state that enters the block's tile of step i
+      float h[1];
+      const int tile = (at.steps - 1 - i) * at.cs + at.rank;
+      row_get<1>(i >= skip && i < at.steps ? carry : nullptr, tile, p.D, ch, h);
+      return h[0];
+    };
+    float mu[1], H = entering(0);
+    row_get<1>(p.ds_final, at.n, p.D, ch, mu);
+    for (int i = 0; i < at.steps; i++) {
+      const float next = entering(i + 1);
+      __syncthreads();  // every warp has folded its chunks of the step
+      glr_chain<false>(&own[0][0], H, lane, true, enter);
+      maps.wait(i);
+      for (int r = at.cs - 1; r >= 0; r--)
+        mu[0] = glr_chain<true>(maps.at(i) + r * kGlrChunks * kGlrSlab, mu[0], lane,
+                                r == at.rank, enter_mu);
+      __syncthreads();
+      if (i > skip) issue();  // every warp is done with the stage of step i - 1
+      H = next;
+    }
+    if (p.d_h0 && at.rank == 0 && ch < p.D) p.d_h0[(int64_t)at.n * p.D + ch] = mu[0];
+    if (maps.late && p.error) atomicOr(p.error, kErrTimeout);
+    __syncwarp();
+    if (at.cs > 1) cg::this_cluster().sync();
     return;
   }
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int ch = (slab * 32 + lane) * V;
-  const bool live = ch < p.D;
-  const int64_t L = (int64_t)p.cu[n + 1] - p.cu[n];
-  const IN* x = static_cast<const IN*>(p.x) + (int64_t)p.cu[n] * p.ldx + ch;
-  const G* g = static_cast<const G*>(p.g) + (int64_t)p.cu[n] * p.ldg + ch;
-  const OUT* dh = static_cast<const OUT*>(p.d_h) + (int64_t)p.cu[n] * p.lddh + ch;
-  IN* dx = static_cast<IN*>(p.d_x) + (int64_t)p.cu[n] * p.lddx + ch;
-  G* dg = static_cast<G*>(p.d_g) + (int64_t)p.cu[n] * p.lddg + ch;
-  const int64_t row0 = (int64_t)p.cu[n] / kGlrTile + n;
-
-  float mu[V];
-  row_get<V>(p.ds_final, n, p.D, ch, live, mu);
-  const int64_t ntiles = (L + kGlrTile - 1) / kGlrTile;
-  for (int64_t s = ntiles - 1; s >= 0; s--) {
-    const int64_t t0 = s * kGlrTile + w * kGlrChunk;
-    typename Raw<IN, V>::type rx[kGlrChunk];
-    typename Raw<OUT, V>::type rd[kGlrChunk];
-    float ga[kGlrChunk][V], H[V], Hm[V], A[V], B[V], M[V];
-    unsigned low = 0;
-    row_get<V>(p.carry, row0 + s, p.D, ch, live, H);
-#pragma unroll
-    for (int t = 0; t < kGlrChunk; t++) {
-      typename Raw<G, V>::type rg;
-      raw_zero(rx[t]);
-      raw_zero(rd[t]);
-      raw_zero(rg);
-      if (live && t0 + t < L) {
-        rx[t] = raw_load<IN, V>(x + (t0 + t) * p.ldx);
-        rd[t] = raw_load<OUT, V>(dh + (t0 + t) * p.lddh);
-        rg = raw_load<G, V>(g + (t0 + t) * p.ldg);
+  const IN* x = static_cast<const IN*>(p.x) + (int64_t)at.start * p.ldx + at.ch;
+  const G* g = static_cast<const G*>(p.g) + (int64_t)at.start * p.ldg + at.ch;
+  const OUT* dh = static_cast<const OUT*>(p.d_h) + (int64_t)at.start * p.lddh + at.ch;
+  IN* dx = static_cast<IN*>(p.d_x) + (int64_t)at.start * p.lddx + at.ch;
+  G* dg = static_cast<G*>(p.d_g) + (int64_t)at.start * p.lddg + at.ch;
+  for (int i = 0; i < at.steps; i++) {
+    const int tile = (at.steps - 1 - i) * at.cs + at.rank;
+    const int t0 = tile * kGlrTile + at.c * kGlrChunk;
+    const int tokens = chunk_tokens(at, t0), have = at.live ? tokens : 0;
+    float ga[kGlrChunk][V], A[kGlrChunk][V], B[kGlrChunk][V], M[V], mm[V], Hm[V];
+    unsigned far = 0;
+    GlrSource<IN, V, STAGED> sx;
+    GlrSource<G, V, STAGED> sg;
+    GlrSource<OUT, V, STAGED> sd;
+    if (i >= skip) {
+      if constexpr (STAGED) {
+        sx.set(stage[pipe.slot].x, at);
+        sg.set(stage[pipe.slot].g, at);
+        sd.set(stage[pipe.slot].dh, at);
+        pipe.wait();
+        pipe.next();
+        if (tokens < kGlrChunk) {
+          sx.clear_from(tokens);
+          sg.clear_from(tokens);
+          sd.clear_from(tokens);
+          fence_async_smem();  // the stage is copied into again
+        }
+      } else {
+        sg.load(g + (int64_t)t0 * p.ldg, p.ldg, have);
+        sx.load(x + (int64_t)t0 * p.ldx, p.ldx, have);
+        sd.load(dh + (int64_t)t0 * p.lddh, p.lddh, have);
       }
-      widen(rg, ga[t]);
-    }
 #pragma unroll
-    for (int v = 0; v < V; v++) {
-      A[v] = 1.f;
-      B[v] = M[v] = 0.f;
-    }
+      for (int t = 0; t < kGlrChunk; t++) {
+        float xv[V], gv[V], dv[V];
+        widen(sx.get(t), xv);
+        widen(sg.get(t), gv);
+        widen(sd.get(t), dv);
 #pragma unroll
-    for (int t = 0; t < kGlrChunk; t++) {
-      float xv[V];
-      widen(rx[t], xv);
+        for (int v = 0; v < V; v++) {
+          ga[t][v] = gate_of<MODE>(gv[v], far, t * V + v);
+          const float a = gate_a<MODE>(ga[t][v], far, t * V + v);
+          const float b = gate_b<MODE>(ga[t][v], far, t * V + v, xv[v]);
+          A[t][v] = t ? __fmul_rn(a, A[t - 1][v]) : a;
+          B[t][v] = t ? __fmaf_rn(a, B[t - 1][v], b) : __fmaf_rn(a, 0.f, b);
+          M[v] = t ? __fmaf_rn(A[t][v], dv[v], M[v]) : __fmul_rn(a, dv[v]);
+        }
+      }
+    } else {  // only in a cluster's first step: this block's tile is behind the end
 #pragma unroll
       for (int v = 0; v < V; v++) {
-        ga[t][v] = gate_of<MODE>(ga[t][v], low, t * V + v);
-        const float a = gate_a<MODE>(ga[t][v], low, t * V + v);
-        A[v] = __fmul_rn(a, A[v]);
-        B[v] = __fmaf_rn(a, B[v], gate_b<MODE>(ga[t][v], low, t * V + v, xv[v]));
+        A[kGlrChunk - 1][v] = 1.f;
+        B[kGlrChunk - 1][v] = M[v] = 0.f;
       }
     }
+    maps.expect(i);
+    glr_share<V>(maps, i, at, A[kGlrChunk - 1], M);
 #pragma unroll
-    for (int t = kGlrChunk - 1; t >= 0; t--) {
-      float dv[V];
-      widen(rd[t], dv);
-#pragma unroll
-      for (int v = 0; v < V; v++)
-        M[v] = __fmul_rn(gate_a<MODE>(ga[t][v], low, t * V + v), __fadd_rn(dv[v], M[v]));
-    }
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-      sA[s & 1][w][lane * V + v] = A[v];
-      sB[s & 1][w][lane * V + v] = B[v];
-      sM[s & 1][w][lane * V + v] = M[v];
-    }
+    for (int v = 0; v < V; v++)
+      own[at.c][at.col + v] = make_float2(A[kGlrChunk - 1][v], B[kGlrChunk - 1][v]);
     __syncthreads();
-    float mm[V];
-#pragma unroll
-    for (int i = 0; i < kGlrWarps; i++)
-#pragma unroll
-      for (int v = 0; v < V; v++) {
-        if (i == w) Hm[v] = H[v];
-        H[v] = __fmaf_rn(sA[s & 1][i][lane * V + v], H[v], sB[s & 1][i][lane * V + v]);
-      }
-#pragma unroll
-    for (int i = kGlrWarps - 1; i >= 0; i--)
-#pragma unroll
-      for (int v = 0; v < V; v++) {
-        if (i == w) mm[v] = mu[v];
-        mu[v] = __fmaf_rn(sA[s & 1][i][lane * V + v], mu[v], sM[s & 1][i][lane * V + v]);
-      }
-    if (!live || t0 >= L) continue;
-    float hp[kGlrChunk][V];  // h_{t-1}
+    __syncthreads();  // the service warp has handed over
+    if (have == 0) continue;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      A[v] = 1.f;
-      B[v] = 0.f;
+      Hm[v] = enter[at.c][at.col + v];
+      mm[v] = enter_mu[at.c][at.col + v];
     }
-#pragma unroll
-    for (int t = 0; t < kGlrChunk; t++) {
-      float xv[V];
-      widen(rx[t], xv);
+    IN* ox = dx + (int64_t)t0 * p.lddx;
+    G* og = dg + (int64_t)t0 * p.lddg;
+    auto back = [&](int t, bool write) {
+      float dv[V], xv[V], fx[V], fg[V];
+      widen(sd.get(t), dv);
+      widen(sx.get(t), xv);
 #pragma unroll
       for (int v = 0; v < V; v++) {
-        hp[t][v] = __fmaf_rn(A[v], Hm[v], B[v]);
-        const float a = gate_a<MODE>(ga[t][v], low, t * V + v);
-        A[v] = __fmul_rn(a, A[v]);
-        B[v] = __fmaf_rn(a, B[v], gate_b<MODE>(ga[t][v], low, t * V + v, xv[v]));
-      }
-    }
-#pragma unroll
-    for (int t = kGlrChunk - 1; t >= 0; t--) {
-      float dv[V], xv[V], ox[V], og[V];
-      widen(rd[t], dv);
-      widen(rx[t], xv);
-#pragma unroll
-      for (int v = 0; v < V; v++) {
+        const float before = t ? __fmaf_rn(A[t ? t - 1 : 0][v], Hm[v], B[t ? t - 1 : 0][v]) : Hm[v];
         const float lam = __fadd_rn(dv[v], mm[v]);
-        mm[v] = __fmul_rn(gate_a<MODE>(ga[t][v], low, t * V + v), lam);
-        ox[v] = gate_b<MODE>(ga[t][v], low, t * V + v, lam);
-        og[v] = __fmul_rn(mm[v], MODE == GDN_GLR_INPUT_COMPLEMENT ? __fsub_rn(hp[t][v], xv[v])
-                                                                  : hp[t][v]);
+        mm[v] = __fmul_rn(gate_a<MODE>(ga[t][v], far, t * V + v), lam);
+        fx[v] = gate_b<MODE>(ga[t][v], far, t * V + v, lam);
+        fg[v] = __fmul_rn(mm[v], MODE == GDN_GLR_INPUT_COMPLEMENT ? __fsub_rn(before, xv[v])
+                                                                  : before);
       }
-      if (t0 + t < L) {
-        put(dx + (t0 + t) * p.lddx, ox);
-        put(dg + (t0 + t) * p.lddg, og);
+      if (write) {
+        put(row_at(ox, p.lddx, t), fx);
+        put(row_at(og, p.lddg, t), fg);
       }
+    };
+    if (have == kGlrChunk) {
+#pragma unroll
+      for (int t = kGlrChunk - 1; t >= 0; t--) back(t, true);
+    } else {
+#pragma unroll
+      for (int t = kGlrChunk - 1; t >= 0; t--) back(t, t < have);
     }
   }
-  if (p.d_h0 && live && w == 0) put(p.d_h0 + (int64_t)n * p.D + ch, mu);
+  if (pipe.late && p.error) atomicOr(p.error, kErrTimeout);
+  if (at.cs > 1) {  // nothing is on its way to a block that ends
+    __syncwarp();
+    cg::this_cluster().sync();
+  }
 }
 
 // One block per row (a row's pos is read and written by one block).
@@ -418,7 +840,7 @@ constexpr int kGlrStepThreads = 1024;
 template <class IN, class G, class OUT, int V, int MODE>
 __global__ void __launch_bounds__(kGlrStepThreads) k_glr_step(const GlrArgs p) {
   const int b = blockIdx.x;
-  const int slot = glr_slot(p.slot_idx, b, p.st.n_slots);
+  const int slot = glr_slot_block(p.slot_idx, b, p.st.n_slots);
   const int pos = slot < 0 ? -1 : p.st.pos[slot];
   if (pos < 0 || pos >= kGlrChunk) {
     if (threadIdx.x == 0) atomicOr(p.st.error, kErrPos);
@@ -440,10 +862,10 @@ __global__ void __launch_bounds__(kGlrStepThreads) k_glr_step(const GlrArgs p) {
     widen(raw_load<float, V>(p.st.b + base + ch), B);
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      unsigned low = 0;
-      const float wv = gate_of<MODE>(gv[v], low, 0), a = gate_a<MODE>(wv, low, 0);
+      unsigned far = 0;
+      const float wv = gate_of<MODE>(gv[v], far, 0), a = gate_a<MODE>(wv, far, 0);
       A[v] = __fmul_rn(a, pos ? A[v] : 1.f);
-      B[v] = __fmaf_rn(a, pos ? B[v] : 0.f, gate_b<MODE>(wv, low, 0, xv[v]));
+      B[v] = __fmaf_rn(a, pos ? B[v] : 0.f, gate_b<MODE>(wv, far, 0, xv[v]));
       hv[v] = __fmaf_rn(A[v], H[v], B[v]);
       if (full) {
         A[v] = 1.f;
@@ -462,28 +884,110 @@ __global__ void __launch_bounds__(kGlrStepThreads) k_glr_step(const GlrArgs p) {
 // ----------------------------------------------------------------------------
 enum GlrOp { kGlrFwd, kGlrBwd, kGlrStep };
 
-template <class IN, class G, class OUT, int V, int MODE>
-static cudaError_t glr_launch(GlrOp op, GlrArgs& p, cudaStream_t st) {
-  p.slabs = (p.D + 32 * V - 1) / (32 * V);
-  if (op == kGlrStep) {
-    k_glr_step<IN, G, OUT, V, MODE><<<(unsigned)p.N, kGlrStepThreads, 0, st>>>(p);
-  } else {
-    const unsigned blocks = (unsigned)p.N * (unsigned)p.slabs;
-    if (op == kGlrFwd)
-      k_glr_forward<IN, G, OUT, V, MODE><<<blocks, kGlrThreads, 0, st>>>(p);
-    else
-      k_glr_backward<IN, G, OUT, V, MODE><<<blocks, kGlrThreads, 0, st>>>(p);
+// Launch shape.  Blocks of a cluster: doubled while every block of the grid
+// still has a place on the device and a sequence has tiles for them on average.
+// Stages: as many as the shared memory of a multiprocessor holds for the
+// blocks that it gets.
+struct GlrShape {
+  int cs, stages;
+  size_t smem;
+};
+
+static GlrShape glr_shape(const GlrArgs& p, size_t stage, int most) {
+  constexpr int64_t kSms = 148;
+  constexpr size_t kSmem = 228 * 1024, kBlock = 1024 + 4 * 1024;  // of an SM; fixed per block
+  auto maps = [](int cs) { return (size_t)2 * cs * kGlrChunks * kGlrSlab * sizeof(float2) + 128; };
+  auto places = [&](int cs) {
+    const int64_t n = kSmem / (kBlock + maps(cs) + 2 * stage);
+    return kSms * (n < most ? n : most);
+  };
+  const int64_t units = (int64_t)p.N * p.slabs;
+  GlrShape sh{1, 0, 0};
+  while (sh.cs < kGlrMaxCluster && units * 2 * sh.cs <= places(2 * sh.cs) &&
+         p.T > (int64_t)p.N * kGlrTile * sh.cs)
+    sh.cs *= 2;
+  if (stage > 0) {
+    int64_t here = (units * sh.cs + kSms - 1) / kSms;
+    here = here < most ? here : most;
+    const size_t fixed = kBlock + maps(sh.cs);
+    while (here > 1 && kSmem / here < fixed + 2 * stage) here--;
+    sh.stages = (int)((kSmem / here - fixed) / stage);
+    if (sh.stages > kGlrMaxStages) sh.stages = kGlrMaxStages;
   }
-  return cudaGetLastError();
+  sh.smem = sh.stages * stage + maps(sh.cs);
+  return sh;
+}
+
+template <class K>
+static cudaError_t glr_run(K kernel, int threads, size_t stage, int most, GlrArgs& p,
+                           const GlrBoxes& box, cudaStream_t st) {
+  const GlrShape sh = glr_shape(p, stage, most);
+  p.stages = sh.stages;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sh.smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)sh.cs;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)p.N * (unsigned)p.slabs * (unsigned)sh.cs);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = sh.smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, box);
+}
+
+// A map over [T][D] rows of stride ld whose boxes are one tile of one slab;
+// columns past D and tokens past T read as zeros.
+template <class T>
+static bool glr_encode(CUtensorMap* map, const void* base, int64_t tokens, int D, int ld) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || (reinterpret_cast<uintptr_t>(base) & 15) || (size_t)ld * sizeof(T) % 16) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)tokens};
+  const cuuint64_t stride[1] = {(cuuint64_t)ld * sizeof(T)};
+  const cuuint32_t box[2] = {kGlrSlab, kGlrTile}, one[2] = {1, 1};
+  return fn(map,
+            sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+            2, const_cast<void*>(base), dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class IN, class G, class OUT, int MODE>
+static cudaError_t glr_launch(GlrOp op, GlrArgs& p, bool pairs, cudaStream_t st) {
+  p.slabs = (p.D + kGlrSlab - 1) / kGlrSlab;
+  if (op == kGlrStep) {
+    if (pairs)
+      k_glr_step<IN, G, OUT, 2, MODE><<<(unsigned)p.N, kGlrStepThreads, 0, st>>>(p);
+    else
+      k_glr_step<IN, G, OUT, 1, MODE><<<(unsigned)p.N, kGlrStepThreads, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  GlrBoxes box{};
+  // pairs: the rows that are written take two elements at a time
+  const bool staged = pairs && p.T > 0 && glr_encode<IN>(&box.x, p.x, p.T, p.D, p.ldx) &&
+                      glr_encode<G>(&box.g, p.g, p.T, p.D, p.ldg) &&
+                      (op == kGlrFwd || glr_encode<OUT>(&box.dh, p.d_h, p.T, p.D, p.lddh));
+  if (op == kGlrFwd) {
+    if (staged)
+      return glr_run(k_glr_forward<IN, G, OUT, 2, MODE, true>, kGlrBlock<2>,
+                     sizeof(GlrForwardStage<IN, G>), glr_blocks<2>(true), p, box, st);
+    return glr_run(k_glr_forward<IN, G, OUT, 1, MODE, false>, kGlrBlock<1>, 0, glr_blocks<1>(op == kGlrFwd), p, box, st);
+  }
+  if (staged)
+    return glr_run(k_glr_backward<IN, G, OUT, 2, MODE, true>, kGlrBlock<2>,
+                   sizeof(GlrBackwardStage<IN, G, OUT>), glr_blocks<2>(false), p, box, st);
+  return glr_run(k_glr_backward<IN, G, OUT, 1, MODE, false>, kGlrBlock<1>, 0, glr_blocks<1>(op == kGlrFwd), p, box, st);
 }
 
 template <class IN, class G, class OUT>
 static cudaError_t glr_modes(GlrOp op, GlrArgs& p, bool pairs, int mode, cudaStream_t st) {
   if (mode == GDN_GLR_INPUT_PLAIN)
-    return pairs ? glr_launch<IN, G, OUT, 2, GDN_GLR_INPUT_PLAIN>(op, p, st)
-                 : glr_launch<IN, G, OUT, 1, GDN_GLR_INPUT_PLAIN>(op, p, st);
-  return pairs ? glr_launch<IN, G, OUT, 2, GDN_GLR_INPUT_COMPLEMENT>(op, p, st)
-               : glr_launch<IN, G, OUT, 1, GDN_GLR_INPUT_COMPLEMENT>(op, p, st);
+    return glr_launch<IN, G, OUT, GDN_GLR_INPUT_PLAIN>(op, p, pairs, st);
+  return glr_launch<IN, G, OUT, GDN_GLR_INPUT_COMPLEMENT>(op, p, pairs, st);
 }
 
 static cudaError_t glr_types(GlrOp op, GlrArgs& p, bool ib, bool gb, bool ob, bool pairs,
@@ -512,7 +1016,8 @@ bool valid_dtype(int d) { return d == GDN_BF16 || d == GDN_F32; }
 size_t size_of(int dtype) { return dtype == GDN_BF16 ? 2 : 4; }
 
 constexpr int kMaxD = 1 << 24;
-constexpr int64_t kMaxLd = (int64_t)1 << 40;  // rows x stride stays far inside 64 bits
+constexpr int64_t kMaxTokens = INT32_MAX - (1 << 12);  // a last step's tiles stay in 32 bits
+constexpr int64_t kMaxLd = (int64_t)1 << 27;  // a chunk's offsets fit 32 bits
 
 // One strided matrix: present, element-aligned, stride in range.
 int check_rows(const void* p, int64_t ld, int dtype, int D) {
@@ -543,17 +1048,17 @@ int check_state(const gdn_glr_state& st) {
 // Checks shared by forward and backward.
 int check_batch(const int32_t* cu, int n_seqs, int64_t T, int D, const int32_t* error_word) {
   if (n_seqs < 0 || T < 0 || !aligned(error_word, 4)) return GDN_ERR_INVALID_ARG;
-  if (T > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if (T > kMaxTokens) return GDN_ERR_UNSUPPORTED;
   if (n_seqs == 0) return T == 0 ? GDN_OK : GDN_ERR_INVALID_ARG;
   if (!cu || !aligned(cu, 4)) return GDN_ERR_INVALID_ARG;
-  const int64_t blocks = (int64_t)n_seqs * ((D + 31) / 32);
-  return blocks > INT32_MAX ? GDN_ERR_UNSUPPORTED : GDN_OK;
+  const int64_t blocks = (int64_t)n_seqs * ((D + 31) / 32);  // clusters of up to 8
+  return blocks * 8 > INT32_MAX ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }
 
 }  // namespace
 
 extern "C" int64_t gdn_glr_carry_rows(int n_seqs, int64_t total_tokens) {
-  if (n_seqs < 0 || total_tokens < 0 || total_tokens > INT32_MAX) return 0;
+  if (n_seqs < 0 || total_tokens < 0 || total_tokens > kMaxTokens) return 0;
   return total_tokens / GDN_GLR_TILE + n_seqs;
 }
 
@@ -582,21 +1087,22 @@ extern "C" int gdn_glr_forward(const void* x, int64_t ldx, int in_dtype, const v
     if (!slot_idx && n_seqs > state->n_slots) return GDN_ERR_INVALID_ARG;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (error_word && cudaMemsetAsync(error_word, 0, sizeof(int32_t), st) != cudaSuccess)
-    return GDN_ERR_CUDA;
-  if (n_seqs == 0) return GDN_OK;
+  if (n_seqs == 0)
+    return !error_word || cudaMemsetAsync(error_word, 0, sizeof(int32_t), st) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
   gdn::GlrArgs p{};
   p.x = x;
   p.g = g;
-  p.ldx = ldx;
-  p.ldg = ldg;
+  p.ldx = (int)ldx;
+  p.ldg = (int)ldg;
   p.cu = cu_seqlens;
   p.N = n_seqs;
-  p.T = total_tokens;
+  p.T = (int)total_tokens;
   p.D = D;
   p.h0 = h0;
   p.h = h;
-  p.ldh = ldh;
+  p.ldh = (int)ldh;
   p.s_final = s_final;
   if (state) p.st = *state;
   p.slot_idx = slot_idx;
@@ -632,26 +1138,27 @@ extern "C" int gdn_glr_backward(const void* x, int64_t ldx, int in_dtype, const 
   if (!aligned(carry, 16) || !aligned(ds_final, 16) || !aligned(d_h0, 16))
     return GDN_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (error_word && cudaMemsetAsync(error_word, 0, sizeof(int32_t), st) != cudaSuccess)
-    return GDN_ERR_CUDA;
-  if (n_seqs == 0) return GDN_OK;
+  if (n_seqs == 0)
+    return !error_word || cudaMemsetAsync(error_word, 0, sizeof(int32_t), st) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
   gdn::GlrArgs p{};
   p.x = x;
   p.g = g;
-  p.ldx = ldx;
-  p.ldg = ldg;
+  p.ldx = (int)ldx;
+  p.ldg = (int)ldg;
   p.cu = cu_seqlens;
   p.N = n_seqs;
-  p.T = total_tokens;
+  p.T = (int)total_tokens;
   p.D = D;
   p.carry = const_cast<float*>(carry);
   p.d_h = d_h;
-  p.lddh = lddh;
+  p.lddh = (int)lddh;
   p.ds_final = ds_final;
   p.d_x = d_x;
-  p.lddx = lddx;
+  p.lddx = (int)lddx;
   p.d_g = d_g;
-  p.lddg = lddg;
+  p.lddg = (int)lddg;
   p.d_h0 = d_h0;
   p.error = error_word;
   return gdn::glr_types(gdn::kGlrBwd, p, in_dtype == GDN_BF16, g_dtype == GDN_BF16,
@@ -679,12 +1186,12 @@ extern "C" int gdn_glr_decode_step(const void* x, int64_t ldx, int in_dtype, con
   gdn::GlrArgs p{};
   p.x = x;
   p.g = g;
-  p.ldx = ldx;
-  p.ldg = ldg;
+  p.ldx = (int)ldx;
+  p.ldg = (int)ldg;
   p.N = B;
   p.D = D;
   p.h = h;
-  p.ldh = ldh;
+  p.ldh = (int)ldh;
   p.st = state;
   p.slot_idx = slot_idx;
   return gdn::glr_types(gdn::kGlrStep, p, in_dtype == GDN_BF16, g_dtype == GDN_BF16,
