@@ -20,7 +20,8 @@
  *
  * Sums are fp32 in a fixed order for each head, so a head's bits depend on
  * that head, its position and the weights alone: prefill, training and
- * decode agree bit for bit whatever the batch.  Angles are reduced in fp64
+ * decode agree bit for bit whatever the batch.  (Another rotation of the same
+ * head may give its norm's sum another order.)  Angles are reduced in 64 bits
  * before the fp32 sine and cosine.
  *
  * Conventions are those of gdn_cpr.h.  q and k are [tokens, heads, d] with

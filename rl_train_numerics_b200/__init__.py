@@ -11,7 +11,10 @@ __all__ = ["gdn", "workloads", "build_lib"]
 
 def __getattr__(name):
     if name == "gdn":
-        return importlib.import_module("rl_train_numerics_b200._abi")
-    if name in ("workloads", "build_lib"):
-        return importlib.import_module(f"rl_train_numerics_b200.{name}")
-    raise AttributeError(name)
+        module = importlib.import_module("rl_train_numerics_b200._abi")
+    elif name in ("workloads", "build_lib"):
+        module = importlib.import_module(f"rl_train_numerics_b200.{name}")
+    else:
+        raise AttributeError(name)
+    globals()[name] = module  # found without this function from now on
+    return module

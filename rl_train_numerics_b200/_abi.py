@@ -480,17 +480,24 @@ def chunk_boundary(s_start, k, v, beta, g, *, s_end=None, stream=None):
 # entry points see bare pointers.
 
 class _Call:
-    """Device, stream and checks of one call."""
+    """Device, stream and checks of one call.  (These run in front of kernels of a few
+    microseconds: messages are put together only when a check has failed.)"""
 
-    def __init__(self, what: str, dev: torch.device, stream):
-        if dev.type != "cuda":
+    __slots__ = ("what", "index", "dev", "user_stream", "raw")
+
+    def __init__(self, what: str, t: torch.Tensor, stream):
+        if not t.is_cuda:
             raise ValueError("gdn_cpr: tensors must be on a CUDA device (there is no CPU path)")
-        self.what, self.dev = what, dev
-        self.index = dev.index
+        self.what = what
+        self.dev = t.device
+        self.index = t.get_device()
         self.user_stream = stream
-        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
-        if self.stream.device_index != self.index:
-            raise ValueError(f"{what}: stream and tensors are on different devices")
+        if stream is None:
+            self.raw = torch._C._cuda_getCurrentRawStream(self.index)
+        else:
+            self.raw = stream.cuda_stream
+            self.need(stream.device_index == self.index,
+                      "stream and tensors are on different devices")
 
     def need(self, ok: bool, why: str):
         if not ok:
@@ -510,30 +517,36 @@ class _Call:
         """Address of a contiguous tensor (None stays NULL)."""
         if t is None:
             return None
-        self.need(t.device == self.dev, f"{name} is on {t.device}, not {self.dev}")
-        self.need(t.dtype == dtype, f"{name} must be {dtype}")
-        self.need(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}")
-        self.need(t.is_contiguous(), f"{name} must be contiguous")
+        if (t.get_device() != self.index or t.dtype != dtype or t.shape != shape
+                or not t.is_contiguous()):
+            self.need(t.device == self.dev, f"{name} is on {t.device}, not {self.dev}")
+            self.need(t.dtype == dtype, f"{name} must be {dtype}")
+            self.need(t.shape == shape, f"{name} must have shape {tuple(shape)}")
+            self.need(False, f"{name} must be contiguous")
         return t.data_ptr()
 
     def rows(self, t, name: str, shape, dtype=None):
         """Address and row stride of [T, ...] whose rows are contiguous."""
-        self.need(t.device == self.dev, f"{name} is on {t.device}, not {self.dev}")
-        self.need(dtype is None or t.dtype == dtype, f"{name} must be {dtype}")
-        self.need(t.shape == shape, f"{name} must have shape {tuple(shape)}")
-        width = 1
-        for n, step in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-            self.need(n <= 1 or step == width, f"the rows of {name} must be contiguous")
-            width *= n
-        return t.data_ptr(), (t.stride(0) if shape[0] > 1 else width)
+        if t.get_device() != self.index or t.shape != shape or (dtype is not None
+                                                                and t.dtype != dtype):
+            self.need(t.device == self.dev, f"{name} is on {t.device}, not {self.dev}")
+            self.need(t.shape == shape, f"{name} must have shape {tuple(shape)}")
+            self.need(False, f"{name} must be {dtype}")
+        step, width = t.stride(), 1
+        for i in range(len(shape) - 1, 0, -1):
+            if step[i] != width and shape[i] > 1:
+                self.need(False, f"the rows of {name} must be contiguous")
+            width *= shape[i]
+        return t.data_ptr(), (step[0] if shape[0] > 1 else width)
 
     def run(self, fn, *args):
-        if self.index == torch.cuda.current_device():
-            st = fn(*args, self.stream.cuda_stream)
+        if self.index == torch._C._cuda_getDevice():
+            st = fn(*args, self.raw)
         else:
-            with torch.cuda.device(self.dev):
-                st = fn(*args, self.stream.cuda_stream)
-        _check(st, self.what)
+            with torch.cuda.device(self.index):
+                st = fn(*args, self.raw)
+        if st != GDN_OK:
+            raise GdnError(st, self.what)
 
 
 def _dtype_of(code_or_dtype, default):
@@ -554,7 +567,7 @@ def _qk_call(what, q, k, norm, wq, wk, positions, inv_freq, stream):
     some = q if q is not None else k
     if some is None or any(t is not None and t.dim() != 3 for t in (q, k)):
         raise ValueError(f"{what}: q, k must be [tokens, heads, d] (one of them may be None)")
-    c = _Call(what, some.device, stream)
+    c = _Call(what, some, stream)
     T, _, d = some.shape
     Hq = 0 if q is None else q.shape[1]
     Hk = 0 if k is None else k.shape[1]
@@ -718,7 +731,7 @@ def glr_forward(x, g, cu_seqlens, *, n_seqs: Optional[int] = None, h0=None,
     strided; h0, s_final [N, D] fp32.  ``state`` (and slot_idx) receives the
     decode state of every sequence; want_carry=True returns the fp32 rows that
     glr_backward needs.  Returns (h, s_final, carry, error word)."""
-    c = _Call("gdn_glr_forward", x.device, stream)
+    c = _Call("gdn_glr_forward", x, stream)
     c.need(x.dim() == 2 and g.dim() == 2, "x, g must be [tokens, channels]")
     T, D = x.shape
     ins = _glr_inputs(c, x, g)
@@ -751,7 +764,7 @@ def glr_backward(x, g, cu_seqlens, carry, d_h, *, n_seqs: Optional[int] = None, 
     ``carry``; d_h [T, D] (bf16 or fp32).  Returns (grads, error word); grads is
     a dict of dx, dg [T, D] (the dtypes of x and g) and dh0 [N, D] fp32 (None
     unless want_dh0).  Pass ``grads`` (the same dict) to reuse buffers."""
-    c = _Call("gdn_glr_backward", x.device, stream)
+    c = _Call("gdn_glr_backward", x, stream)
     c.need(x.dim() == 2 and g.dim() == 2, "x, g must be [tokens, channels]")
     T, D = x.shape
     ins = _glr_inputs(c, x, g)
@@ -777,7 +790,7 @@ def glr_decode_step(state: GlrDecodeState, x, g, *, slot_idx=None, complement: b
                     out_dtype=None, h=None, stream=None):
     """gdn_glr_decode_step for B rows: x, g [B, D]; row b advances slot slot_idx[b]
     (int32; slot b without it).  Returns h [B, D]; bad rows set state.error."""
-    c = _Call("gdn_glr_decode_step", x.device, stream)
+    c = _Call("gdn_glr_decode_step", x, stream)
     c.need(x.dim() == 2 and g.dim() == 2, "x, g must be [rows, channels]")
     B, D = x.shape
     ins = _glr_inputs(c, x, g)

@@ -1,13 +1,16 @@
 // gdn_qk_norm.cu -- norms of queries and keys for each head with the position
 // rotation in the same pass, and their gradients (gdn_qk_norm.h).
 //
-// A head of D channels lies on D / 8 lanes, eight neighbouring channels each;
-// its sum of squares is a sum over those eight in ascending order and a
-// butterfly over the lanes, so a head's bits are its own.  A block takes a
-// few tokens and all their heads: the angles' cosines and sines are computed
-// once for a token into shared memory and serve every head.  A rotated pair
-// (j, j + F) lies on two lanes F / 8 apart (one shuffle), an interleaved pair
-// on one.
+// A group of D / 8 lanes has a head's D channels, each lane two pieces of four
+// neighbouring ones.  With pairs (j, j + F) the pieces of a lane are a rotated
+// pair, so that the rotation needs no exchange; the lanes behind the rotated
+// channels, and all lanes otherwise, have eight neighbours.  Sums over a head
+// are the lane's two packed partial sums, added, and a butterfly over the
+// group: a head's bits are its own.
+//
+// A group takes some heads of one token at a time: the token's cosines and
+// sines, computed once by the group's lanes and exchanged, stay in registers
+// with the weights, and the loads of several heads are under way together.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -17,22 +20,20 @@
 namespace gdn {
 
 constexpr int kQkThreads = 256;
-constexpr int kQkMaxTokens = 16;      // tokens of a block's angle table
-constexpr int kQkWeightBlocks = 592;  // most partial sums of a weight's gradient
 
 enum QkRot { kRotNone = 0, kRotHalves = 1, kRotPairs = 2 };
 
 struct QkSide {
   const void* x;
-  int64_t ldx;
-  const float* w;
-  void* y;
-  int64_t ldy;
   const void* dy;
-  int64_t lddy;
-  void* dx;
-  int64_t lddx;
+  const float* w;
+  void* out;  // y, or dx
+  int64_t ldx, lddy, ldout;
   int H;
+  int heads;   // of a unit: one token's heads that a group takes at a time
+  int chunks;  // units of a token
+  int64_t blocks;  // that the grid has for this side (q's first)
+  int64_t span;    // units of one block
 };
 
 struct QkArgs {
@@ -40,244 +41,343 @@ struct QkArgs {
   int64_t T;
   const int32_t* positions;
   const float* inv_freq;
-  int F;            // rotated pairs
-  int tokens;       // of one table
-  int64_t span;     // tokens of one block
+  int F;             // rotated pairs
   float eps, inv_m;  // inv_m: 1 (l2) or 1 / D (rms)
-  float* partial;   // [blocks][2][D] or nullptr
+  float* partial;    // [blocks][D] or nullptr
 };
 
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0];
-  const float4 b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+// Four neighbouring channels as loaded.
+template <class T>
+struct Four;
+template <>
+struct Four<float> {
+  using type = float4;
+};
+template <>
+struct Four<__nv_bfloat16> {
+  using type = uint2;
+};
+
+// A lane's eight channels as packed pairs.
+struct Eight {
+  float2 v[4];
+};
+__device__ __forceinline__ void widen4(const float4& r, float2* v) {
+  v[0] = f2(r.x, r.y);
+  v[1] = f2(r.z, r.w);
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
-  const unsigned u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
+__device__ __forceinline__ void widen4(const uint2& r, float2* v) {
+  v[0] = f2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u));
+  v[1] = f2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
 }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store4(float* p, const float2* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float2* v) {
   union {
-    uint4 r;
-    __nv_bfloat162 h[4];
+    uint2 r;
+    __nv_bfloat162 h[2];
   } u;
-#pragma unroll
-  for (int i = 0; i < 4; i++) u.h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-  *reinterpret_cast<uint4*>(p) = u.r;
+  u.h[0] = __floats2bfloat162_rn(v[0].x, v[0].y);
+  u.h[1] = __floats2bfloat162_rn(v[1].x, v[1].y);
+  *reinterpret_cast<uint2*>(p) = u.r;
 }
 
-// Cosine and sine of pos * f.  The angle is taken in quarter turns in fp64
-// (an fp32 product has lost the angle from positions of a few thousand on)
-// and the nearest quarter removed, so that the fp32 functions see at most an
-// eighth of a turn.
-__device__ __forceinline__ float2 angle(int pos, float f) {
-  const double quarters = (double)pos * ((double)f * 0.63661977236758134308);  // 2 / pi
-  const double whole = rint(quarters);
+// Angles are counted in turns, as fractions of 2^64: pos times a frequency wraps
+// around by itself, which is the reduction that a far position needs (an fp32
+// product has lost the angle from positions of a few thousand on).  The
+// frequency comes from an fp64 product, the upper 32 bits of the angle are
+// kept, and the nearest quarter turn is taken off, so that the fp32 functions
+// see at most an eighth of a turn.
+__device__ __forceinline__ uint64_t frequency(float f) {
+  double turns = (double)f * 0.15915494309189533577;  // 1 / 2 pi
+  turns -= floor(turns);
+  return (uint64_t)(turns * 18446744073709551616.0);  // 2^64
+}
+__device__ __forceinline__ float2 angle(int pos, uint64_t f) {
+  const uint32_t t = (uint32_t)(((uint64_t)(int64_t)pos * f) >> 32);
+  const uint32_t quarter = (t + (1u << 29)) >> 30;
   float s, c;
-  sincospif(0.5f * (float)(quarters - whole), &s, &c);
-  const int turn = (int)((long long)whole & 3);
-  if (turn & 1) {
-    const float x = c;
-    c = -s;
-    s = x;
-  }
-  return turn & 2 ? make_float2(-c, -s) : make_float2(c, s);
+  sincospif((float)(int32_t)(t - (quarter << 30)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+  const float x = quarter & 1 ? -s : c, y = quarter & 1 ? c : s;
+  return quarter & 2 ? f2(-x, -y) : f2(x, y);
 }
 
-__device__ __forceinline__ void angle_table(const QkArgs& p, int64_t t0, int nt, float* cs,
-                                            float* sn) {
-  for (int e = threadIdx.x; e < nt * p.F; e += kQkThreads) {
-    const int t = e / p.F, j = e - t * p.F;
-    const float2 a = angle(p.positions[t0 + t], p.inv_freq[j]);
-    cs[e] = a.x;
-    sn[e] = a.y;
+// Where a lane stands in its head: its pieces' first channels, and the first of
+// its angles (-1: its channels are not rotated).
+struct QkLane {
+  int lane;  // in the group
+  int a, b;
+  int angle;
+};
+template <int D, int ROT>
+__device__ __forceinline__ QkLane qk_lane(int F) {
+  QkLane l;
+  l.lane = threadIdx.x % (D / 8);
+  l.a = 8 * l.lane;
+  l.angle = -1;
+  if (ROT == kRotHalves && l.lane < F / 4) {
+    l.a = l.angle = 4 * l.lane;
+    l.b = l.a + F;
+  } else {
+    l.b = l.a + 4;
+    if (ROT == kRotPairs && l.a < 2 * F) l.angle = l.a / 2;
   }
+  return l;
 }
 
-// Rotate the eight channels from c0 on by the angles at cs, sn (SIGN = -1:
-// back).  Every lane of the warp calls this.
-template <int ROT, int SIGN>
-__device__ __forceinline__ void rotate8(float (&n)[8], int c0, int F, const float* cs,
-                                        const float* sn) {
-  if (ROT == kRotHalves) {
-    const bool first = c0 < F, in = c0 < 2 * F;
-    const int lane = threadIdx.x & 31;
-    const int src = in ? (first ? lane + F / 8 : lane - F / 8) : lane;
-    const int j = first ? c0 : c0 - F;
+// The angles of a token for a group: its lanes share the work, and each reads
+// its four.  All lanes of a warp call it (`have`: the group has a token).
+template <int D, int ROT>
+__device__ __forceinline__ void qk_angles(const QkArgs& p, const QkLane& l, bool have, int64_t t,
+                                          const uint64_t* freq, float2* table,
+                                          float2 (&turn)[4]) {
+  if (ROT == kRotNone) return;
+  __syncwarp();  // the last token's have been read
+  if (have) {
+    const int pos = p.positions[t];
+    for (int j = l.lane; j < p.F; j += D / 8) table[j] = angle(pos, freq[j]);
+  }
+  __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const float other = __shfl_sync(kFull, n[i], src);
-      if (in) {
-        const float s = (first ? -SIGN : SIGN) * sn[j + i];
-        n[i] = __fmaf_rn(other, s, __fmul_rn(n[i], cs[j + i]));
-      }
+  for (int i = 0; i < 4; i++) turn[i] = l.angle >= 0 ? table[l.angle + i] : f2(1.f, 0.f);
+}
+
+// Rotate a lane's channels (SIGN = -1: back).
+template <int ROT, int SIGN>
+__device__ __forceinline__ void rotate8(Eight& n, const QkLane& l, const float2 (&turn)[4]) {
+  if (ROT == kRotNone || l.angle < 0) return;
+  if (ROT == kRotHalves) {
+    const float2 c[2] = {f2(turn[0].x, turn[1].x), f2(turn[2].x, turn[3].x)};
+    const float2 s[2] = {f2(SIGN * turn[0].y, SIGN * turn[1].y),
+                         f2(SIGN * turn[2].y, SIGN * turn[3].y)};
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const float2 u = n.v[i], v = n.v[2 + i];
+      n.v[i] = __ffma2_rn(f2(-v.x, -v.y), s[i], __fmul2_rn(u, c[i]));
+      n.v[2 + i] = __ffma2_rn(u, s[i], __fmul2_rn(v, c[i]));
     }
-  } else if (ROT == kRotPairs && c0 < 2 * F) {
+  } else {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      const float c = cs[c0 / 2 + i], s = SIGN * sn[c0 / 2 + i];
-      const float u = n[2 * i], v = n[2 * i + 1];
-      n[2 * i] = __fmaf_rn(-v, s, __fmul_rn(u, c));
-      n[2 * i + 1] = __fmaf_rn(u, s, __fmul_rn(v, c));
+      const float u = n.v[i].x, v = n.v[i].y, c = turn[i].x, s = SIGN * turn[i].y;
+      n.v[i].x = __fmaf_rn(-v, s, __fmul_rn(u, c));
+      n.v[i].y = __fmaf_rn(u, s, __fmul_rn(v, c));
     }
   }
 }
 
 template <int D>
-__device__ __forceinline__ float head_sum(float s) {
+__device__ __forceinline__ float dot8(const Eight& a, const Eight& b) {
+  float2 s = __fmul2_rn(a.v[0], b.v[0]);
 #pragma unroll
-  for (int m = 1; m < D / 8; m *= 2) s = __fadd_rn(s, __shfl_xor_sync(kFull, s, m));
-  return s;
+  for (int i = 1; i < 4; i++) s = __ffma2_rn(a.v[i], b.v[i], s);
+  float t = __fadd_rn(s.x, s.y);
+#pragma unroll
+  for (int m = 1; m < D / 8; m *= 2) t = __fadd_rn(t, __shfl_xor_sync(kFull, t, m));
+  return t;
+}
+__device__ __forceinline__ void scale8(Eight& n, float r) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) n.v[i] = __fmul2_rn(n.v[i], f2(r, r));
+}
+__device__ __forceinline__ void times8(Eight& n, const Eight& w) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) n.v[i] = __fmul2_rn(n.v[i], w.v[i]);
+}
+__device__ __forceinline__ void weights8(const float* w, const QkLane& l, Eight& f) {
+  widen4(*reinterpret_cast<const float4*>(w + l.a), f.v);
+  widen4(*reinterpret_cast<const float4*>(w + l.b), f.v + 2);
 }
 
-template <int D>
-__device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
-  float s = __fmul_rn(a[0], b[0]);
-#pragma unroll
-  for (int i = 1; i < 8; i++) s = __fmaf_rn(a[i], b[i], s);
-  return head_sum<D>(s);
+// The unit (token, first head) of a group in one pass of its block.
+struct QkUnit {
+  bool have;
+  int64_t t;
+  int h0, heads;
+};
+__device__ __forceinline__ QkUnit qk_unit(const QkSide& sd, int64_t u, int64_t end) {
+  QkUnit q;
+  q.have = u < end;
+  q.t = q.have ? u / sd.chunks : 0;
+  q.h0 = q.have ? (int)(u - q.t * sd.chunks) * sd.heads : 0;
+  q.heads = q.have ? min(sd.heads, sd.H - q.h0) : 0;
+  return q;
 }
 
-template <int D>
-__device__ __forceinline__ void weights8(const float* w, int c0, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; i++) f[i] = 1.f;
-  if (w) load8(w + c0, f);
+// Heads whose loads are under way together, and the blocks of a multiprocessor
+// that their registers are kept to.  10240 x (16 + 16) heads of 128, no
+// rotation: forward 28 us with 4 heads and 5 blocks (2 heads: 31), backward 57 us
+// with 2 heads and 3 blocks (4 heads and 2 blocks: 64, 1 and 4: 68).  16384 x
+// (32 + 8) rotated with weights: forward 66 us (78 without the bound), backward
+// 113 us with 4 heads and 2 blocks (2 and 3: 119, 1 and 4: 131).
+constexpr int kQkForwardBatch = 4;
+__host__ __device__ constexpr int qk_forward_blocks(int rot, size_t element) {
+  return rot == kRotNone ? 5 : element == 2 ? 4 : 3;
 }
+__host__ __device__ constexpr int qk_backward_batch(int rot) { return rot == kRotNone ? 2 : 4; }
+__host__ __device__ constexpr int qk_backward_blocks(int rot) { return rot == kRotNone ? 3 : 2; }
 
 template <class IN, class OUT, int D, int ROT>
-__global__ void __launch_bounds__(kQkThreads) k_qk_forward(const QkArgs p) {
-  constexpr int kLanes = D / 8, kGroups = kQkThreads / kLanes;
-  extern __shared__ float smem[];
-  float *cs = smem, *sn = smem + p.tokens * p.F;
-  const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
-  const int nt = (int)min((int64_t)p.tokens, p.T - t0);
+__global__ void __launch_bounds__(kQkThreads, qk_forward_blocks(ROT, sizeof(IN)))
+    k_qk_forward(const QkArgs p) {
+  constexpr int kLanes = D / 8, kGroups = kQkThreads / kLanes, kBatch = kQkForwardBatch;
+  extern __shared__ uint64_t freq[];  // [F], and each group's [F] cosines and sines
+  const bool isq = blockIdx.x < p.q.blocks;
+  const QkSide& sd = isq ? p.q : p.k;
+  const int64_t first = (isq ? blockIdx.x : blockIdx.x - p.q.blocks) * sd.span;
+  const int64_t end = min(first + sd.span, p.T * sd.chunks);
+  const int grp = threadIdx.x / kLanes;
+  const QkLane l = qk_lane<D, ROT>(p.F);
+  float2* table = reinterpret_cast<float2*>(freq + p.F) + grp * p.F;
   if (ROT != kRotNone) {
-    angle_table(p, t0, nt, cs, sn);
+    for (int j = threadIdx.x; j < p.F; j += kQkThreads) freq[j] = frequency(p.inv_freq[j]);
     __syncthreads();
   }
-  const int grp = threadIdx.x / kLanes, c0 = (threadIdx.x % kLanes) * 8;
-  const int heads = p.q.H + p.k.H, items = nt * heads;
-  float wq[8], wk[8];
-  weights8<D>(p.q.w, c0, wq);
-  weights8<D>(p.k.w, c0, wk);
-  for (int first = 0; first < items; first += kGroups) {
-    const int it = first + grp;
-    const bool have = it < items;
-    const int t = have ? it / heads : 0, hd = have ? it - t * heads : 0;
-    const bool isq = hd < p.q.H;
-    const QkSide& sd = isq ? p.q : p.k;
-    const int64_t ch = (int64_t)(isq ? hd : hd - p.q.H) * D + c0;
-    float n[8] = {};
-    if (have) load8(static_cast<const IN*>(sd.x) + (t0 + t) * sd.ldx + ch, n);
-    const float r =
-        __frsqrt_rn(__fmaf_rn(dot8<D>(n, n), p.inv_m, p.eps));
+  Eight w;
+  if (sd.w) weights8(sd.w, l, w);
+  using Raw4 = typename Four<IN>::type;
+  for (int64_t base = first; base < end; base += kGroups) {
+    const QkUnit u = qk_unit(sd, base + grp, end);
+    const IN* x = static_cast<const IN*>(sd.x) + u.t * sd.ldx + (int64_t)u.h0 * D;
+    OUT* y = static_cast<OUT*>(sd.out) + u.t * sd.ldout + (int64_t)u.h0 * D;
+    float2 turn[4];
+    Raw4 ra[kBatch] = {}, rb[kBatch] = {};
+    auto load = [&](int h) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) n[i] = __fmul_rn(__fmul_rn(n[i], r), isq ? wq[i] : wk[i]);
-    rotate8<ROT, 1>(n, c0, p.F, cs + t * p.F, sn + t * p.F);
-    if (have) store8(static_cast<OUT*>(sd.y) + (t0 + t) * sd.ldy + ch, n);
+      for (int i = 0; i < kBatch; i++)
+        if (h + i < u.heads) {
+          ra[i] = *reinterpret_cast<const Raw4*>(x + (h + i) * D + l.a);
+          rb[i] = *reinterpret_cast<const Raw4*>(x + (h + i) * D + l.b);
+        }
+    };
+    load(0);  // under way while the angles are computed
+    qk_angles<D, ROT>(p, l, u.have, u.t, freq, table, turn);
+    // The warp's groups go through as many heads as the one with most.
+    for (int h = 0; h < sd.heads; h += kBatch) {
+      if (h > 0) load(h);
+#pragma unroll
+      for (int i = 0; i < kBatch; i++) {
+        if (h + i >= sd.heads) break;
+        Eight n;
+        widen4(ra[i], n.v);
+        widen4(rb[i], n.v + 2);
+        scale8(n, __frsqrt_rn(__fmaf_rn(dot8<D>(n, n), p.inv_m, p.eps)));
+        if (sd.w) times8(n, w);
+        rotate8<ROT, 1>(n, l, turn);
+        if (h + i < u.heads) {
+          store4(y + (h + i) * D + l.a, n.v);
+          store4(y + (h + i) * D + l.b, n.v + 2);
+        }
+      }
+    }
   }
 }
 
 template <class IN, class GR, int D, int ROT>
-__device__ __forceinline__ void qk_backward_side(const QkArgs& p, const QkSide& sd, int64_t t0,
-                                                 int nt, const float* cs, const float* sn,
-                                                 float (&dw)[8]) {
-  constexpr int kLanes = D / 8, kGroups = kQkThreads / kLanes;
-  const int grp = threadIdx.x / kLanes, c0 = (threadIdx.x % kLanes) * 8;
-  const int items = nt * sd.H;
-  float w[8];
-  weights8<D>(sd.w, c0, w);
-  for (int first = 0; first < items; first += kGroups) {
-    const int it = first + grp;
-    const bool have = it < items;
-    const int t = have ? it / sd.H : 0;
-    const int64_t ch = (int64_t)(have ? it - t * sd.H : 0) * D + c0;
-    float x[8] = {}, e[8] = {};
-    if (have) {
-      load8(static_cast<const IN*>(sd.x) + (t0 + t) * sd.ldx + ch, x);
-      load8(static_cast<const GR*>(sd.dy) + (t0 + t) * sd.lddy + ch, e);
-    }
-    rotate8<ROT, -1>(e, c0, p.F, cs + t * p.F, sn + t * p.F);
-    const float r = __frsqrt_rn(__fmaf_rn(dot8<D>(x, x), p.inv_m, p.eps));
+__global__ void __launch_bounds__(kQkThreads, qk_backward_blocks(ROT))
+    k_qk_backward(const QkArgs p) {
+  constexpr int kLanes = D / 8, kGroups = kQkThreads / kLanes, kBatch = qk_backward_batch(ROT);
+  extern __shared__ uint64_t freq[];  // [F], and each group's [F] cosines and sines
+  const bool isq = blockIdx.x < p.q.blocks;
+  const QkSide& sd = isq ? p.q : p.k;
+  const int64_t first = (isq ? blockIdx.x : blockIdx.x - p.q.blocks) * sd.span;
+  const int64_t end = min(first + sd.span, p.T * sd.chunks);
+  const int grp = threadIdx.x / kLanes;
+  const QkLane l = qk_lane<D, ROT>(p.F);
+  float2* table = reinterpret_cast<float2*>(freq + p.F) + grp * p.F;
+  if (ROT != kRotNone) {
+    for (int j = threadIdx.x; j < p.F; j += kQkThreads) freq[j] = frequency(p.inv_freq[j]);
+    __syncthreads();
+  }
+  Eight w, dw;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      dw[i] = __fmaf_rn(e[i], __fmul_rn(x[i], r), dw[i]);
-      e[i] = __fmul_rn(e[i], w[i]);
-    }
-    const float m = __fmul_rn(dot8<D>(x, e), p.inv_m);
-    const float z = __fmul_rn(__fmul_rn(r, r), m);
+  for (int i = 0; i < 4; i++) dw.v[i] = f2(0.f, 0.f);
+  if (sd.w) weights8(sd.w, l, w);
+  using RawX = typename Four<IN>::type;
+  using RawG = typename Four<GR>::type;
+  for (int64_t base = first; base < end; base += kGroups) {
+    const QkUnit u = qk_unit(sd, base + grp, end);
+    const IN* x = static_cast<const IN*>(sd.x) + u.t * sd.ldx + (int64_t)u.h0 * D;
+    const GR* dy = static_cast<const GR*>(sd.dy) + u.t * sd.lddy + (int64_t)u.h0 * D;
+    IN* dx = static_cast<IN*>(sd.out) + u.t * sd.ldout + (int64_t)u.h0 * D;
+    float2 turn[4];
+    RawX xa[kBatch] = {}, xb[kBatch] = {};
+    RawG ga[kBatch] = {}, gb[kBatch] = {};
+    auto load = [&](int h) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) e[i] = __fmul_rn(r, __fmaf_rn(-x[i], z, e[i]));
-    if (have) store8(static_cast<IN*>(sd.dx) + (t0 + t) * sd.lddx + ch, e);
+      for (int i = 0; i < kBatch; i++) {
+        const bool here = h + i < u.heads;
+        xa[i] = here ? *reinterpret_cast<const RawX*>(x + (h + i) * D + l.a) : RawX{};
+        xb[i] = here ? *reinterpret_cast<const RawX*>(x + (h + i) * D + l.b) : RawX{};
+        ga[i] = here ? *reinterpret_cast<const RawG*>(dy + (h + i) * D + l.a) : RawG{};
+        gb[i] = here ? *reinterpret_cast<const RawG*>(dy + (h + i) * D + l.b) : RawG{};
+      }
+    };
+    load(0);
+    qk_angles<D, ROT>(p, l, u.have, u.t, freq, table, turn);
+    for (int h = 0; h < sd.heads; h += kBatch) {
+      if (h > 0) load(h);
+#pragma unroll
+      for (int i = 0; i < kBatch; i++) {
+        if (h + i >= sd.heads) break;
+        Eight n, e;  // the head and its gradient (zeros for a group without one)
+        widen4(xa[i], n.v);
+        widen4(xb[i], n.v + 2);
+        widen4(ga[i], e.v);
+        widen4(gb[i], e.v + 2);
+        rotate8<ROT, -1>(e, l, turn);
+        const float r = __frsqrt_rn(__fmaf_rn(dot8<D>(n, n), p.inv_m, p.eps));
+        if (sd.w) {
+          const float2 rr = f2(r, r);
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+            dw.v[j] = __ffma2_rn(e.v[j], __fmul2_rn(n.v[j], rr), dw.v[j]);
+          times8(e, w);
+        }
+        const float m = __fmul_rn(dot8<D>(n, e), p.inv_m);
+        const float z = -__fmul_rn(__fmul_rn(r, r), m);
+#pragma unroll
+        for (int j = 0; j < 4; j++) e.v[j] = __ffma2_rn(n.v[j], f2(z, z), e.v[j]);
+        scale8(e, r);
+        if (h + i < u.heads) {
+          store4(dx + (h + i) * D + l.a, e.v);
+          store4(dx + (h + i) * D + l.b, e.v + 2);
+        }
+      }
+    }
+  }
+  if (p.partial && sd.w) {  // the block's sum of dw over its groups, in ascending order
+    __shared__ float red[kGroups][D];
+    store4(&red[grp][l.a], dw.v);
+    store4(&red[grp][l.b], dw.v + 2);
+    __syncthreads();
+    for (int c = threadIdx.x; c < D; c += kQkThreads) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < kGroups; j++) s = __fadd_rn(s, red[j][c]);
+      p.partial[(int64_t)blockIdx.x * D + c] = s;
+    }
   }
 }
 
-// The block's sum of dw over its groups, in ascending order.
-template <int D>
-__device__ __forceinline__ void weight_partial(const float (&dw)[8], float* red, float* out) {
-  constexpr int kLanes = D / 8, kGroups = kQkThreads / kLanes;
-  const int grp = threadIdx.x / kLanes, c0 = (threadIdx.x % kLanes) * 8;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 8; i++) red[grp * D + c0 + i] = dw[i];
-  __syncthreads();
-  for (int c = threadIdx.x; c < D; c += kQkThreads) {
-    float s = 0.f;
-    for (int j = 0; j < kGroups; j++) s = __fadd_rn(s, red[j * D + c]);
-    out[c] = s;
-  }
-}
-
-template <class IN, class GR, int D, int ROT>
-__global__ void __launch_bounds__(kQkThreads) k_qk_backward(const QkArgs p) {
-  extern __shared__ float smem[];
-  float *cs = smem, *sn = smem + p.tokens * p.F;
-  float dwq[8] = {}, dwk[8] = {};
-  const int64_t begin = (int64_t)blockIdx.x * p.span, end = min(p.T, begin + p.span);
-  for (int64_t t0 = begin; t0 < end; t0 += p.tokens) {
-    const int nt = (int)min((int64_t)p.tokens, end - t0);
-    if (ROT != kRotNone) {
-      if (t0 != begin) __syncthreads();  // the last tokens' angles have been read
-      angle_table(p, t0, nt, cs, sn);
-      __syncthreads();
-    }
-    qk_backward_side<IN, GR, D, ROT>(p, p.q, t0, nt, cs, sn, dwq);
-    qk_backward_side<IN, GR, D, ROT>(p, p.k, t0, nt, cs, sn, dwk);
-  }
-  if (p.partial) {
-    __shared__ float red[kQkThreads * 8];
-    float* out = p.partial + (int64_t)blockIdx.x * 2 * D;
-    weight_partial<D>(dwq, red, out);
-    weight_partial<D>(dwk, red, out + D);
-  }
-}
-
-// d_w = sum of the blocks' partial sums: row group r of 8 adds the blocks
-// r, r + 8, ... in order, then the groups are added in order.
-__global__ void __launch_bounds__(256) k_qk_weight_sum(const float* partial, int blocks, int D,
-                                                       float* d_wq, float* d_wk) {
-  __shared__ float red[8][32];
+// d_w = sum of the blocks' partial sums (y: the side): row group r of 32 adds
+// the blocks r, r + 32, ... in order, then the groups are added in order.
+__global__ void __launch_bounds__(1024)
+    k_qk_weight_sum(const float* partial, int q_blocks, int k_blocks, int D, float* d_wq,
+                    float* d_wk) {
+  __shared__ float red[32][32];
   float* out = blockIdx.y == 0 ? d_wq : d_wk;
   if (!out) return;
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
-  const float* col = partial + blockIdx.y * D + c;
+  const int blocks = blockIdx.y == 0 ? q_blocks : k_blocks;
+  const float* col = partial + (blockIdx.y == 0 ? 0 : (int64_t)q_blocks * D) + c;
   float s = 0.f;
-  for (int b = r; b < blocks; b += 8) s = __fadd_rn(s, col[(int64_t)b * 2 * D]);
+  for (int b = r; b < blocks; b += 32) s = __fadd_rn(s, col[(int64_t)b * D]);
   red[r][threadIdx.x & 31] = s;
   __syncthreads();
   if (r == 0) {
-    for (int j = 1; j < 8; j++) s = __fadd_rn(s, red[j][threadIdx.x]);
+    for (int j = 1; j < 32; j++) s = __fadd_rn(s, red[j][threadIdx.x]);
     out[c] = s;
   }
 }
@@ -285,69 +385,80 @@ __global__ void __launch_bounds__(256) k_qk_weight_sum(const float* partial, int
 // ----------------------------------------------------------------------------
 // Launchers
 // ----------------------------------------------------------------------------
-struct QkPlan {
-  int tokens;
-  int64_t span, blocks;
-};
+// Heads of a unit and blocks of each side.  A unit has up to 32 heads (what it
+// spends on the angles is shared by them), fewer while the units would not fill
+// the device (kQkFill lane groups).  A block takes one unit for each of its
+// groups; where it keeps a partial sum of a weight's gradient (`sums`: about
+// how many there are to be) it takes its share of its side, so that all blocks
+// run at once.  The plan depends on sizes alone, so the sums' order does not
+// change from device to device.  False when the grid would be too large.
+constexpr int kQkUnitHeads = 32;
+constexpr int kQkFill = 148 * 4 * 8;
 
-// Tokens of a block: about four heads for each of its lane groups, fewer
-// while the batch would leave multiprocessors idle.
-static int qk_tokens(int64_t T, int heads, int d) {
+static int qk_sums(int rot) { return 148 * qk_backward_blocks(rot); }
+
+static bool qk_plan(QkArgs& p, int64_t T, int Hq, int Hk, int d, int sums) {
+  p.T = T;
+  p.q.H = Hq;
+  p.k.H = Hk;
   const int groups = kQkThreads / (d / 8);
-  int n = 4 * groups / heads;
-  n = n < 1 ? 1 : n > kQkMaxTokens ? kQkMaxTokens : n;
-  while (n > 1 && (T + n - 1) / n < kQkWeightBlocks) n /= 2;
-  return n;
-}
-
-static QkPlan qk_plan(int64_t T, int heads, int d, bool weights) {
-  QkPlan pl;
-  pl.tokens = qk_tokens(T, heads, d);
-  pl.span = pl.tokens;
-  if (weights) {
-    const int64_t per = (T + kQkWeightBlocks - 1) / kQkWeightBlocks;
-    pl.span = (per + pl.tokens - 1) / pl.tokens * pl.tokens;
+  int heads = kQkUnitHeads;
+  while (heads > 1 && T * (Hq + Hk) / heads < kQkFill) heads /= 2;
+  for (QkSide* s : {&p.q, &p.k}) {
+    s->chunks = (s->H + heads - 1) / heads;
+    s->heads = s->chunks > 0 ? (s->H + s->chunks - 1) / s->chunks : 0;  // even shares
+    const int64_t units = T * s->chunks;
+    int64_t passes = 1;
+    if (sums) {
+      const int64_t share = sums * (int64_t)s->H / (Hq + Hk);
+      const int64_t blocks = (units + groups - 1) / groups;
+      passes = share > 0 ? (blocks + share - 1) / share : blocks;
+      if (passes < 1) passes = 1;
+    }
+    s->span = passes * groups;
+    s->blocks = (units + s->span - 1) / s->span;
   }
-  pl.blocks = (T + pl.span - 1) / pl.span;
-  return pl;
+  return p.q.blocks + p.k.blocks <= INT32_MAX;
 }
 
-static size_t qk_smem(const QkArgs& p, int rot) {
-  return rot == kRotNone ? 0 : (size_t)2 * p.tokens * p.F * sizeof(float);
+static size_t qk_smem(const QkArgs& p, int d, int rot) {
+  return rot == kRotNone ? 0 : (size_t)(kQkThreads / (d / 8) + 1) * p.F * sizeof(float2);
 }
 
 template <class IN, class OTHER, int D, int ROT>
-static cudaError_t qk_launch(bool backward, const QkArgs& p, int64_t blocks, cudaStream_t st) {
+static cudaError_t qk_launch(bool backward, const QkArgs& p, cudaStream_t st) {
+  const unsigned blocks = (unsigned)(p.q.blocks + p.k.blocks);
+  const size_t smem = qk_smem(p, D, ROT);
   if (backward)
-    k_qk_backward<IN, OTHER, D, ROT><<<(unsigned)blocks, kQkThreads, qk_smem(p, ROT), st>>>(p);
+    k_qk_backward<IN, OTHER, D, ROT><<<blocks, kQkThreads, smem, st>>>(p);
   else
-    k_qk_forward<IN, OTHER, D, ROT><<<(unsigned)blocks, kQkThreads, qk_smem(p, ROT), st>>>(p);
+    k_qk_forward<IN, OTHER, D, ROT><<<blocks, kQkThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
 template <class IN, class OTHER, int D>
-static cudaError_t qk_rot(bool bwd, const QkArgs& p, int rot, int64_t n, cudaStream_t st) {
-  if (rot == kRotNone) return qk_launch<IN, OTHER, D, kRotNone>(bwd, p, n, st);
-  if (rot == kRotHalves) return qk_launch<IN, OTHER, D, kRotHalves>(bwd, p, n, st);
-  return qk_launch<IN, OTHER, D, kRotPairs>(bwd, p, n, st);
+static cudaError_t qk_rot(bool bwd, const QkArgs& p, int rot, cudaStream_t st) {
+  if (rot == kRotNone) return qk_launch<IN, OTHER, D, kRotNone>(bwd, p, st);
+  if (rot == kRotHalves) return qk_launch<IN, OTHER, D, kRotHalves>(bwd, p, st);
+  return qk_launch<IN, OTHER, D, kRotPairs>(bwd, p, st);
 }
 
 template <class IN, class OTHER>
-static cudaError_t qk_dims(bool bwd, const QkArgs& p, int d, int rot, int64_t n,
+static cudaError_t qk_dims(bool bwd, const QkArgs& p, int d, int rot,
                            cudaStream_t st) {
-  if (d == 64) return qk_rot<IN, OTHER, 64>(bwd, p, rot, n, st);
-  if (d == 128) return qk_rot<IN, OTHER, 128>(bwd, p, rot, n, st);
-  return qk_rot<IN, OTHER, 256>(bwd, p, rot, n, st);
+  if (d == 64) return qk_rot<IN, OTHER, 64>(bwd, p, rot, st);
+  if (d == 128) return qk_rot<IN, OTHER, 128>(bwd, p, rot, st);
+  return qk_rot<IN, OTHER, 256>(bwd, p, rot, st);
 }
 
 static cudaError_t qk_types(bool bwd, const QkArgs& p, bool ib, bool ob, int d, int rot,
-                            int64_t n, cudaStream_t st) {
+                            cudaStream_t st) {
   using bf16 = __nv_bfloat16;
   if (ib)
-    return ob ? qk_dims<bf16, bf16>(bwd, p, d, rot, n, st)
-              : qk_dims<bf16, float>(bwd, p, d, rot, n, st);
-  return ob ? qk_dims<float, bf16>(bwd, p, d, rot, n, st)
-            : qk_dims<float, float>(bwd, p, d, rot, n, st);
+    return ob ? qk_dims<bf16, bf16>(bwd, p, d, rot, st)
+              : qk_dims<bf16, float>(bwd, p, d, rot, st);
+  return ob ? qk_dims<float, bf16>(bwd, p, d, rot, st)
+            : qk_dims<float, float>(bwd, p, d, rot, st);
 }
 
 }  // namespace gdn
@@ -411,19 +522,16 @@ extern "C" int gdn_qk_norm_forward(const void* q, int64_t ldq, const void* k, in
   if ((rc = check_heads(oq, ldoq, out_dtype, Hq, d)) != GDN_OK) return rc;
   if ((rc = check_heads(ok, ldok, out_dtype, Hk, d)) != GDN_OK) return rc;
   gdn::QkArgs p{};
-  p.q.x = q, p.q.ldx = ldq, p.q.w = wq, p.q.y = oq, p.q.ldy = ldoq, p.q.H = Hq;
-  p.k.x = k, p.k.ldx = ldk, p.k.w = wk, p.k.y = ok, p.k.ldy = ldok, p.k.H = Hk;
-  p.T = T;
+  if (!gdn::qk_plan(p, T, Hq, Hk, d, 0)) return GDN_ERR_UNSUPPORTED;
+  p.q.x = q, p.q.ldx = ldq, p.q.w = wq, p.q.out = oq, p.q.ldout = ldoq;
+  p.k.x = k, p.k.ldx = ldk, p.k.w = wk, p.k.out = ok, p.k.ldout = ldok;
   p.positions = positions;
   p.inv_freq = inv_freq;
   p.F = rot_dim / 2;
   p.eps = eps;
   p.inv_m = norm == GDN_QK_NORM_RMS ? 1.f / (float)d : 1.f;
-  const gdn::QkPlan pl = gdn::qk_plan(T, Hq + Hk, d, false);
-  p.tokens = pl.tokens;
-  p.span = pl.span;
   return gdn::qk_types(false, p, in_dtype == GDN_BF16, out_dtype == GDN_BF16, d,
-                       rot_kind(rot_dim, interleaved), pl.blocks,
+                       rot_kind(rot_dim, interleaved),
                        static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? GDN_OK
              : GDN_ERR_CUDA;
@@ -431,7 +539,10 @@ extern "C" int gdn_qk_norm_forward(const void* q, int64_t ldq, const void* k, in
 
 extern "C" size_t gdn_qk_norm_backward_workspace_bytes(int64_t T, int Hq, int Hk, int d) {
   if (check_shape(T, Hq, Hk, d) != GDN_OK || T == 0) return 0;
-  return (size_t)gdn::qk_plan(T, Hq + Hk, d, true).blocks * 2 * d * sizeof(float);
+  gdn::QkArgs p{};
+  // (the plan with more sums; a rotation's backward keeps fewer)
+  if (!gdn::qk_plan(p, T, Hq, Hk, d, gdn::qk_sums(gdn::kRotNone))) return 0;
+  return (size_t)(p.q.blocks + p.k.blocks) * d * sizeof(float);
 }
 
 extern "C" int gdn_qk_norm_backward(const void* q, int64_t ldq, const void* k, int64_t ldk,
@@ -462,32 +573,29 @@ extern "C" int gdn_qk_norm_backward(const void* q, int64_t ldq, const void* k, i
   if ((rc = check_heads(d_q, lddq, in_dtype, Hq, d)) != GDN_OK) return rc;
   if ((rc = check_heads(d_k, lddk, in_dtype, Hk, d)) != GDN_OK) return rc;
   const bool weights = d_wq || d_wk;
-  const gdn::QkPlan pl = gdn::qk_plan(T, Hq + Hk, d, weights);
   if (weights) {
     if (!workspace || workspace_bytes < gdn_qk_norm_backward_workspace_bytes(T, Hq, Hk, d))
       return GDN_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return GDN_ERR_INVALID_ARG;
   }
   gdn::QkArgs p{};
-  p.q.x = q, p.q.ldx = ldq, p.q.w = wq, p.q.dy = d_oq, p.q.lddy = lddoq, p.q.dx = d_q;
-  p.q.lddx = lddq, p.q.H = Hq;
-  p.k.x = k, p.k.ldx = ldk, p.k.w = wk, p.k.dy = d_ok, p.k.lddy = lddok, p.k.dx = d_k;
-  p.k.lddx = lddk, p.k.H = Hk;
-  p.T = T;
+  if (!gdn::qk_plan(p, T, Hq, Hk, d, weights ? gdn::qk_sums(rot_kind(rot_dim, interleaved)) : 0)) return GDN_ERR_UNSUPPORTED;
+  p.q.x = q, p.q.ldx = ldq, p.q.w = wq, p.q.dy = d_oq, p.q.lddy = lddoq, p.q.out = d_q;
+  p.q.ldout = lddq;
+  p.k.x = k, p.k.ldx = ldk, p.k.w = wk, p.k.dy = d_ok, p.k.lddy = lddok, p.k.out = d_k;
+  p.k.ldout = lddk;
   p.positions = positions;
   p.inv_freq = inv_freq;
   p.F = rot_dim / 2;
   p.eps = eps;
   p.inv_m = norm == GDN_QK_NORM_RMS ? 1.f / (float)d : 1.f;
-  p.tokens = pl.tokens;
-  p.span = pl.span;
   p.partial = weights ? static_cast<float*>(workspace) : nullptr;
   if (gdn::qk_types(true, p, in_dtype == GDN_BF16, grad_dtype == GDN_BF16, d,
-                    rot_kind(rot_dim, interleaved), pl.blocks, st) != cudaSuccess)
+                    rot_kind(rot_dim, interleaved), st) != cudaSuccess)
     return GDN_ERR_CUDA;
   if (weights) {
-    gdn::k_qk_weight_sum<<<dim3((unsigned)(d / 32), 2), 256, 0, st>>>(p.partial, (int)pl.blocks,
-                                                                      d, d_wq, d_wk);
+    gdn::k_qk_weight_sum<<<dim3((unsigned)(d / 32), 2), 1024, 0, st>>>(
+        p.partial, (int)p.q.blocks, (int)p.k.blocks, d, d_wq, d_wk);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   }
   return GDN_OK;

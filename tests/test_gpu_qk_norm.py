@@ -158,8 +158,7 @@ def test_extreme_values(gdn):
     x, p = f64(q[keep]), f64(kw["positions"])[keep]
     close(oq[keep], qk_norm.forward(x, None, p, f64(kw["inv_freq"])),
           qk_norm.forward_bound(x, None, p, f64(kw["inv_freq"])))
-    plain, _ = gdn.qk_norm_forward(q, k)
-    assert torch.equal(plain[0], oq[0])     # position 0: no turn
+    close(oq[:1], qk_norm.forward(f64(q[:1])), qk_norm.forward_bound(f64(q[:1])))  # no turn
     length = (oq[2, 0].double() ** 2).sum()
     assert abs(float(length) - 1) < 1e-5
 
