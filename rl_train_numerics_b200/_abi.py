@@ -532,12 +532,30 @@ class _Call:
             self.need(t.device == self.dev, f"{name} is on {t.device}, not {self.dev}")
             self.need(t.shape == shape, f"{name} must have shape {tuple(shape)}")
             self.need(False, f"{name} must be {dtype}")
-        step, width = t.stride(), 1
-        for i in range(len(shape) - 1, 0, -1):
-            if step[i] != width and shape[i] > 1:
-                self.need(False, f"the rows of {name} must be contiguous")
-            width *= shape[i]
+        step, width = t.stride(), shape[-1]
+        ok = step[-1] == 1 or width <= 1
+        if len(shape) == 3:
+            ok = ok and (step[1] == width or shape[1] <= 1)
+            width *= shape[1]
+        if not ok:
+            self.need(False, f"the rows of {name} must be contiguous")
         return t.data_ptr(), (step[0] if shape[0] > 1 else width)
+
+    def out_full(self, t, want: bool, name: str, shape, dtype):
+        """An output: the caller's (checked), a new one if wanted, or None."""
+        if t is not None:
+            return t, self.full(t, name, shape, dtype)
+        if not want:
+            return None, None
+        t = self.empty(shape, dtype)
+        return t, t.data_ptr()
+
+    def out_rows(self, t, name: str, shape, dtype):
+        """The same for strided rows, which are always wanted."""
+        if t is not None:
+            return t, *self.rows(t, name, shape, dtype)
+        t = self.empty(shape, dtype)
+        return t, t.data_ptr(), (shape[1] if len(shape) == 2 else shape[1] * shape[2])
 
     def run(self, fn, *args):
         if self.index == torch._C._cuda_getDevice():
@@ -602,9 +620,7 @@ def qk_norm_forward(q, k, *, norm: str = "l2", eps: float = 1e-6, wq=None, wk=No
         if x is None:
             out += [None, None, 0]
             continue
-        if o is None:
-            o = c.empty((T, H, d), odt)
-        out += [o, *c.rows(o, name, (T, H, d), odt)]
+        out += c.out_rows(o, name, (T, H, d), odt)
     c.run(lib.gdn_qk_norm_forward, *head, float(eps), *tail, int(bool(interleaved)), out[1],
           out[2], out[4], out[5], _dtype_code_of(odt))
     return out[0], out[3]
@@ -634,15 +650,14 @@ def qk_norm_backward(q, k, d_oq, d_ok, *, norm: str = "l2", eps: float = 1e-6, w
             res["d" + s] = None
             continue
         gin += [*c.rows(g, "d_o" + s, (T, H, d), gdt)]
-        dx = grads["d" + s] if grads is not None else c.empty((T, H, d), dt)
-        gout += [*c.rows(dx, "d" + s, (T, H, d), dt)]
-        res["d" + s] = dx
+        given = grads["d" + s] if grads is not None else None
+        res["d" + s], *at = c.out_rows(given, "d" + s, (T, H, d), dt)
+        gout += at
     for s, w in (("q", wq), ("k", wk)):
-        dw = None
-        if w is not None and want_dw:
-            dw = grads["dw" + s] if grads is not None else c.empty((d,), torch.float32)
-        gout.append(c.full(dw, "dw" + s, (d,), torch.float32))
-        res["dw" + s] = dw
+        given = grads["dw" + s] if grads is not None and w is not None and want_dw else None
+        res["dw" + s], at = c.out_full(given, w is not None and want_dw, "dw" + s, (d,),
+                                       torch.float32)
+        gout.append(at)
     need = 0
     if res["dwq"] is not None or res["dwk"] is not None:
         need = qk_norm_backward_workspace_bytes(T, Hq, Hk, d)
@@ -737,23 +752,16 @@ def glr_forward(x, g, cu_seqlens, *, n_seqs: Optional[int] = None, h0=None,
     ins = _glr_inputs(c, x, g)
     N, cu = _glr_batch(c, cu_seqlens, n_seqs)
     odt = _dtype_of(out_dtype, h.dtype if h is not None else x.dtype)
-    if h is None:
-        h = c.empty((T, D), odt)
-    hp, ldh = c.rows(h, "h", (T, D), odt)
-    if s_final is None and want_state:
-        s_final = c.empty((N, D), torch.float32)
+    f32 = torch.float32
     rows = glr_carry_rows(N, T)
-    if carry is None and want_carry:
-        carry = c.empty((rows, D), torch.float32)
-    if error is None:
-        error = c.empty((1,), torch.int32)
+    h, hp, ldh = c.out_rows(h, "h", (T, D), odt)
+    s_final, fin = c.out_full(s_final, want_state, "s_final", (N, D), f32)
+    carry, car = c.out_full(carry, want_carry, "carry", (rows, D), f32)
+    error, err = c.out_full(error, True, "error", (1,), torch.int32)
     st = None if state is None else ctypes.byref(_glr_state(c, state, D))
     c.run(lib.gdn_glr_forward, *ins, cu, N, T, D, _glr_mode(complement),
-          c.full(h0, "h0", (N, D), torch.float32), hp, ldh, _dtype_code_of(odt),
-          c.full(s_final, "s_final", (N, D), torch.float32), st,
-          c.full(slot_idx, "slot_idx", (N,), torch.int32),
-          c.full(carry, "carry", (rows, D), torch.float32),
-          c.full(error, "error", (1,), torch.int32))
+          c.full(h0, "h0", (N, D), f32), hp, ldh, _dtype_code_of(odt), fin, st,
+          c.full(slot_idx, "slot_idx", (N,), torch.int32), car, err)
     return h, s_final, carry, error
 
 
@@ -770,19 +778,19 @@ def glr_backward(x, g, cu_seqlens, carry, d_h, *, n_seqs: Optional[int] = None, 
     ins = _glr_inputs(c, x, g)
     N, cu = _glr_batch(c, cu_seqlens, n_seqs)
     dhp, lddh = c.rows(d_h, "d_h", (T, D))
-    if grads is None:
-        grads = {"dx": c.empty((T, D), x.dtype), "dg": c.empty((T, D), g.dtype),
-                 "dh0": c.empty((N, D), torch.float32) if want_dh0 else None}
-    if error is None:
-        error = c.empty((1,), torch.int32)
     c.need(carry is not None, "carry is the forward's (want_carry=True)")
-    c.run(lib.gdn_glr_backward, *ins, cu, N, T, D, _glr_mode(complement),
-          c.full(carry, "carry", (glr_carry_rows(N, T), D), torch.float32), dhp, lddh,
-          _dtype_code(d_h), c.full(ds_final, "ds_final", (N, D), torch.float32),
-          *c.rows(grads["dx"], "dx", (T, D), x.dtype),
-          *c.rows(grads["dg"], "dg", (T, D), g.dtype),
-          c.full(grads.get("dh0"), "dh0", (N, D), torch.float32),
-          c.full(error, "error", (1,), torch.int32))
+    car = c.full(carry, "carry", (glr_carry_rows(N, T), D), torch.float32)
+    given = grads if grads is not None else {}
+    dx, dxp, lddx = c.out_rows(given.get("dx"), "dx", (T, D), x.dtype)
+    dg, dgp, lddg = c.out_rows(given.get("dg"), "dg", (T, D), g.dtype)
+    dh0, dhp0 = c.out_full(given.get("dh0"), want_dh0 and grads is None, "dh0", (N, D),
+                           torch.float32)
+    if grads is None:
+        grads = {"dx": dx, "dg": dg, "dh0": dh0}
+    error, err = c.out_full(error, True, "error", (1,), torch.int32)
+    c.run(lib.gdn_glr_backward, *ins, cu, N, T, D, _glr_mode(complement), car, dhp, lddh,
+          _dtype_code(d_h), c.full(ds_final, "ds_final", (N, D), torch.float32), dxp, lddx, dgp,
+          lddg, dhp0, err)
     return grads, error
 
 
@@ -795,9 +803,7 @@ def glr_decode_step(state: GlrDecodeState, x, g, *, slot_idx=None, complement: b
     B, D = x.shape
     ins = _glr_inputs(c, x, g)
     odt = _dtype_of(out_dtype, h.dtype if h is not None else x.dtype)
-    if h is None:
-        h = c.empty((B, D), odt)
-    hp, ldh = c.rows(h, "h", (B, D), odt)
+    h, hp, ldh = c.out_rows(h, "h", (B, D), odt)
     c.run(lib.gdn_glr_decode_step, *ins, c.full(slot_idx, "slot_idx", (B,), torch.int32), B, D,
           _glr_mode(complement), _glr_state(c, state, D), hp, ldh, _dtype_code_of(odt))
     return h

@@ -38,13 +38,12 @@ constexpr int kGlrChunk = GDN_GLR_CHUNK;
 constexpr int kGlrChunks = 8;   // chunks of a tile
 constexpr int kGlrTile = kGlrChunk * kGlrChunks;
 constexpr int kGlrSlab = 32;    // channels of a block
-constexpr int kGlrMaxCluster = 8;
 constexpr int kGlrMaxStages = 8;
 constexpr int kGlrPolls = 1 << 22;
 // Blocks of a multiprocessor that a kernel's registers leave room for.
 template <int V>
 __host__ __device__ constexpr int glr_blocks(bool forward) {
-  return V == 1 ? 2 : forward ? 4 : 3;
+  return V == 1 ? (forward ? 2 : 1) : 3;
 }
 template <int V>
 constexpr int kGlrThreads = kGlrChunks * kGlrSlab / V;  // that compute
@@ -413,18 +412,23 @@ struct GlrSource<T, V, true> {
 template <class T, int V>
 struct GlrSource<T, V, false> {
   using R = typename Raw<T, V>::type;
-  R r[kGlrChunk];
+  R r[kGlrChunk], next[kGlrChunk];
+  // The loads of the chunk that the step after this one folds.
   __device__ __forceinline__ void load(const T* row, int ld, int have) {
     if (have == kGlrChunk) {
 #pragma unroll
-      for (int t = 0; t < kGlrChunk; t++) r[t] = raw_load<T, V>(row_at(row, ld, t));
+      for (int t = 0; t < kGlrChunk; t++) next[t] = raw_load<T, V>(row_at(row, ld, t));
     } else {
 #pragma unroll
       for (int t = 0; t < kGlrChunk; t++) {
-        raw_zero(r[t]);
-        if (t < have) r[t] = raw_load<T, V>(row_at(row, ld, t));
+        raw_zero(next[t]);
+        if (t < have) next[t] = raw_load<T, V>(row_at(row, ld, t));
       }
     }
+  }
+  __device__ __forceinline__ void take() {
+#pragma unroll
+    for (int t = 0; t < kGlrChunk; t++) r[t] = next[t];
   }
   __device__ __forceinline__ R get(int t) const { return r[t]; }
 };
@@ -556,10 +560,18 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(true))
   const G* g = static_cast<const G*>(p.g) + (int64_t)at.start * p.ldg + at.ch;
   OUT* h = static_cast<OUT*>(p.h) + (int64_t)at.start * p.ldh + at.ch;
   int t0 = at.rank * kGlrTile + at.c * kGlrChunk;
+  GlrSource<IN, V, STAGED> sx;
+  GlrSource<G, V, STAGED> sg;
+  auto load = [&](int t) {  // direct: the chunk at token t, ahead of its fold
+    if constexpr (!STAGED) {
+      const int have = at.live ? chunk_tokens(at, t) : 0;
+      sx.load(x + (int64_t)t * p.ldx, p.ldx, have);
+      sg.load(g + (int64_t)t * p.ldg, p.ldg, have);
+    }
+  };
+  load(t0);
   for (int s = 0; s < at.steps; s++, t0 += step_tokens) {
     const int tokens = chunk_tokens(at, t0), have = at.live ? tokens : 0;
-    GlrSource<IN, V, STAGED> sx;
-    GlrSource<G, V, STAGED> sg;
     if (s < at.tiles) {
       if constexpr (STAGED) {
         sx.set(stage[pipe.slot].x, at);
@@ -570,8 +582,8 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(true))
           sg.clear_from(tokens);
         }
       } else {
-        sx.load(x + (int64_t)t0 * p.ldx, p.ldx, have);
-        sg.load(g + (int64_t)t0 * p.ldg, p.ldg, have);
+        sx.take();
+        sg.take();
       }
 #pragma unroll
       for (int t = 0; t < kGlrChunk; t++) {
@@ -594,6 +606,7 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(true))
         B[kGlrChunk - 1][v] = 0.f;
       }
     }
+    load(t0 + step_tokens);
     maps.expect(s);
     glr_share<V>(maps, s, at, A[kGlrChunk - 1], B[kGlrChunk - 1]);
     __syncthreads();
@@ -716,7 +729,7 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(false))
     for (int i = 0; i < at.steps; i++) {
       const float next = entering(i + 1);
       __syncthreads();  // every warp has folded its chunks of the step
-      glr_chain<false>(&own[0][0], H, lane, true, enter);
+      glr_chain<false>(&own[0][0], H, lane, true, enter);  // (other blocks' maps are on their way)
       maps.wait(i);
       for (int r = at.cs - 1; r >= 0; r--)
         mu[0] = glr_chain<true>(maps.at(i) + r * kGlrChunks * kGlrSlab, mu[0], lane,
@@ -736,15 +749,24 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(false))
   const OUT* dh = static_cast<const OUT*>(p.d_h) + (int64_t)at.start * p.lddh + at.ch;
   IN* dx = static_cast<IN*>(p.d_x) + (int64_t)at.start * p.lddx + at.ch;
   G* dg = static_cast<G*>(p.d_g) + (int64_t)at.start * p.lddg + at.ch;
+  GlrSource<IN, V, STAGED> sx;
+  GlrSource<G, V, STAGED> sg;
+  GlrSource<OUT, V, STAGED> sd;
+  auto load = [&](int t) {  // direct: the chunk at token t, ahead of its fold
+    if constexpr (!STAGED) {
+      const int have = at.live && t >= 0 ? chunk_tokens(at, t) : 0;
+      sg.load(g + (int64_t)t * p.ldg, p.ldg, have);
+      sx.load(x + (int64_t)t * p.ldx, p.ldx, have);
+      sd.load(dh + (int64_t)t * p.lddh, p.lddh, have);
+    }
+  };
+  load(((at.steps - 1) * at.cs + at.rank) * kGlrTile + at.c * kGlrChunk);
   for (int i = 0; i < at.steps; i++) {
     const int tile = (at.steps - 1 - i) * at.cs + at.rank;
     const int t0 = tile * kGlrTile + at.c * kGlrChunk;
     const int tokens = chunk_tokens(at, t0), have = at.live ? tokens : 0;
     float ga[kGlrChunk][V], A[kGlrChunk][V], B[kGlrChunk][V], M[V], mm[V], Hm[V];
     unsigned far = 0;
-    GlrSource<IN, V, STAGED> sx;
-    GlrSource<G, V, STAGED> sg;
-    GlrSource<OUT, V, STAGED> sd;
     if (i >= skip) {
       if constexpr (STAGED) {
         sx.set(stage[pipe.slot].x, at);
@@ -759,9 +781,9 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(false))
           fence_async_smem();  // the stage is copied into again
         }
       } else {
-        sg.load(g + (int64_t)t0 * p.ldg, p.ldg, have);
-        sx.load(x + (int64_t)t0 * p.ldx, p.ldx, have);
-        sd.load(dh + (int64_t)t0 * p.lddh, p.lddh, have);
+        sg.take();
+        sx.take();
+        sd.take();
       }
 #pragma unroll
       for (int t = 0; t < kGlrChunk; t++) {
@@ -786,6 +808,7 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(false))
         B[kGlrChunk - 1][v] = M[v] = 0.f;
       }
     }
+    load(t0 - step_tokens);
     maps.expect(i);
     glr_share<V>(maps, i, at, A[kGlrChunk - 1], M);
 #pragma unroll
@@ -885,32 +908,46 @@ __global__ void __launch_bounds__(kGlrStepThreads) k_glr_step(const GlrArgs p) {
 enum GlrOp { kGlrFwd, kGlrBwd, kGlrStep };
 
 // Launch shape.  Blocks of a cluster: doubled while every block of the grid
-// still has a place on the device and a sequence has tiles for them on average.
-// Stages: as many as the shared memory of a multiprocessor holds for the
-// blocks that it gets.
+// still has a place on the device and a sequence has tiles for them on average
+// (65536 x 2048 alone, forward: 373, 252, 178 us with 1, 2 and 4; 8 have no
+// place and took 303).  A backward step of 8 blocks is slower than two of 4
+// (32768 x 1024: 131 against 115 us).
+//
+// Stages: as many as the shared memory of a multiprocessor holds for the blocks
+// that it gets, and at least two.  A backward cluster would rather have three
+// and fewer blocks: with two its copies start only behind the last step (20000
+// x 1000 in 9 sequences: 84 against 72 us); where blocks are many the others
+// cover that, and three blocks with two stages win (16384 x 2048 in 32: 90
+// against 107 us).
 struct GlrShape {
   int cs, stages;
   size_t smem;
 };
 
-static GlrShape glr_shape(const GlrArgs& p, size_t stage, int most) {
+static GlrShape glr_shape(const GlrArgs& p, size_t stage, int most, bool backward) {
   constexpr int64_t kSms = 148;
-  constexpr size_t kSmem = 228 * 1024, kBlock = 1024 + 4 * 1024;  // of an SM; fixed per block
+  constexpr size_t kSmem = 228 * 1024, kBlock = 1024 + 4608;  // of an SM; fixed per block
   auto maps = [](int cs) { return (size_t)2 * cs * kGlrChunks * kGlrSlab * sizeof(float2) + 128; };
   auto places = [&](int cs) {
     const int64_t n = kSmem / (kBlock + maps(cs) + 2 * stage);
     return kSms * (n < most ? n : most);
   };
   const int64_t units = (int64_t)p.N * p.slabs;
+  const int max_cluster = backward ? 4 : 8;
   GlrShape sh{1, 0, 0};
-  while (sh.cs < kGlrMaxCluster && units * 2 * sh.cs <= places(2 * sh.cs) &&
+  while (sh.cs < max_cluster && units * 2 * sh.cs <= places(2 * sh.cs) &&
          p.T > (int64_t)p.N * kGlrTile * sh.cs)
     sh.cs *= 2;
+  // Sequences of unequal length keep the device waiting for the longest: two
+  // blocks for each then gain more than a second wave of blocks costs (10240
+  // tokens of 2048 channels in 5 sequences, forward and backward: 100 against 145
+  // us where they are uneven, 100 against 86 us where they are equal).
+  if (sh.cs == 1 && p.N > 1 && units <= most * kSms && p.T > (int64_t)p.N * kGlrTile) sh.cs = 2;
   if (stage > 0) {
+    const size_t fixed = kBlock + maps(sh.cs), least = backward && sh.cs > 1 ? 3 : 2;
     int64_t here = (units * sh.cs + kSms - 1) / kSms;
     here = here < most ? here : most;
-    const size_t fixed = kBlock + maps(sh.cs);
-    while (here > 1 && kSmem / here < fixed + 2 * stage) here--;
+    while (here > 1 && kSmem / here < fixed + least * stage) here--;
     sh.stages = (int)((kSmem / here - fixed) / stage);
     if (sh.stages > kGlrMaxStages) sh.stages = kGlrMaxStages;
   }
@@ -919,9 +956,9 @@ static GlrShape glr_shape(const GlrArgs& p, size_t stage, int most) {
 }
 
 template <class K>
-static cudaError_t glr_run(K kernel, int threads, size_t stage, int most, GlrArgs& p,
-                           const GlrBoxes& box, cudaStream_t st) {
-  const GlrShape sh = glr_shape(p, stage, most);
+static cudaError_t glr_run(K kernel, int threads, size_t stage, int most, bool backward,
+                           GlrArgs& p, const GlrBoxes& box, cudaStream_t st) {
+  const GlrShape sh = glr_shape(p, stage, most, backward);
   p.stages = sh.stages;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)sh.smem);
@@ -974,13 +1011,15 @@ static cudaError_t glr_launch(GlrOp op, GlrArgs& p, bool pairs, cudaStream_t st)
   if (op == kGlrFwd) {
     if (staged)
       return glr_run(k_glr_forward<IN, G, OUT, 2, MODE, true>, kGlrBlock<2>,
-                     sizeof(GlrForwardStage<IN, G>), glr_blocks<2>(true), p, box, st);
-    return glr_run(k_glr_forward<IN, G, OUT, 1, MODE, false>, kGlrBlock<1>, 0, glr_blocks<1>(op == kGlrFwd), p, box, st);
+                     sizeof(GlrForwardStage<IN, G>), glr_blocks<2>(true), false, p, box, st);
+    return glr_run(k_glr_forward<IN, G, OUT, 1, MODE, false>, kGlrBlock<1>, 0,
+                   glr_blocks<1>(true), false, p, box, st);
   }
   if (staged)
     return glr_run(k_glr_backward<IN, G, OUT, 2, MODE, true>, kGlrBlock<2>,
-                   sizeof(GlrBackwardStage<IN, G, OUT>), glr_blocks<2>(false), p, box, st);
-  return glr_run(k_glr_backward<IN, G, OUT, 1, MODE, false>, kGlrBlock<1>, 0, glr_blocks<1>(op == kGlrFwd), p, box, st);
+                   sizeof(GlrBackwardStage<IN, G, OUT>), glr_blocks<2>(false), true, p, box, st);
+  return glr_run(k_glr_backward<IN, G, OUT, 1, MODE, false>, kGlrBlock<1>, 0,
+                 glr_blocks<1>(false), true, p, box, st);
 }
 
 template <class IN, class G, class OUT>
