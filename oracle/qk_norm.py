@@ -66,23 +66,24 @@ def backward(x, dy, w=None, positions=None, inv_freq=None, *, norm="l2", eps=1e-
 
 def forward_bound(x, w=None, positions=None, inv_freq=None, *, norm="l2", eps=1e-6,
                   interleaved=False):
-    """Elementwise bound of an fp32 y.  The sum of squares: at most 14 roundings
-    on a path (8 on a lane, 5 between lanes, eps), half of that in r, one for r,
-    two products: 10 U.  A rotation: cosine and sine are off by at most 3 U
-    (one unit in the last place of sincospif, and the rounding of an angle below
-    an eighth of a turn), product and sum 2 U."""
+    """Elementwise bound of an fp32 y.  The sum of squares: at most 11 roundings
+    on a path (5 on a lane, 5 between lanes, eps), half of that in r, two units
+    in the last place (4 U) of rsqrtf, two products: 11.5 U.  A rotation: cosine
+    and sine are off by at most 3 U (one unit in the last place of sincospif, and
+    the rounding of an angle below an eighth of a turn), product and sum 2 U."""
     n = np.asarray(x, np.float64) * _r(np.asarray(x, np.float64), norm, eps)
     if w is not None:
         n = n * np.asarray(w, np.float64)
-    return 16 * U * _mix(n, inv_freq, interleaved) + 1e-36
+    return 17 * U * _mix(n, inv_freq, interleaved) + 1e-36
 
 
 def backward_bound(x, dy, w=None, positions=None, inv_freq=None, *, norm="l2", eps=1e-6,
                    interleaved=False):
     """Elementwise bounds of an fp32 (dx, dw).  With E the size of e: e is off by
-    6 U E (rotation and weight), r by 8 U, r^2 m(x e) by 16 U + 14 U + 6 U and
-    four products, and r once more: 48 U.  dw: a term is off by 16 U, and a sum of
-    K terms by at most K U of their sizes."""
+    6 U E (rotation and weight), r by 9.5 U, m(x e) by 10 U + 6 U, r^2 m(x e) by
+    19 U + 16 U and three products, its product with x and the difference by 2 U,
+    and r once more by 10.5 U: 51 U.  dw: a term is off by 5 U + 10.5 U and a
+    rounding, and a sum of K terms by at most K U of their sizes."""
     x, dy = np.asarray(x, np.float64), np.asarray(dy, np.float64)
     r = _r(x, norm, eps)
     dn = _mix(dy, inv_freq, interleaved)
@@ -90,4 +91,4 @@ def backward_bound(x, dy, w=None, positions=None, inv_freq=None, *, norm="l2", e
     m = (np.abs(x) * e).sum(-1, keepdims=True) / (x.shape[-1] if norm == "rms" else 1)
     terms = (dn * np.abs(x) * r).sum((0, 1))
     K = x.shape[0] * x.shape[1]
-    return 48 * U * r * (e + np.abs(x) * r * r * m) + 1e-36, (16 + K) * U * terms + 1e-36
+    return 51 * U * r * (e + np.abs(x) * r * r * m) + 1e-36, (17 + K) * U * terms + 1e-36

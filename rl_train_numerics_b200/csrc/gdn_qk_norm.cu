@@ -16,6 +16,7 @@
 
 #include "../../include/gdn_qk_norm.h"
 #include "gdn_common.cuh"
+#include "gdn_mma.cuh"
 
 namespace gdn {
 
@@ -126,12 +127,17 @@ __device__ __forceinline__ QkLane qk_lane(int F) {
   return l;
 }
 
+// A lane's four angles: cosines, sines and the sines' negatives as packed pairs.
+struct Turn {
+  float2 c[2], s[2], m[2];
+};
+
 // The angles of a token for a group: its lanes share the work, and each reads
-// its four.  All lanes of a warp call it (`have`: the group has a token).
-template <int D, int ROT>
+// its four (SIGN = -1: to turn back).  All lanes of a warp call it (`have`: the
+// group has a token).
+template <int D, int ROT, int SIGN>
 __device__ __forceinline__ void qk_angles(const QkArgs& p, const QkLane& l, bool have, int64_t t,
-                                          const uint64_t* freq, float2* table,
-                                          float2 (&turn)[4]) {
+                                          const uint64_t* freq, float2* table, Turn& turn) {
   if (ROT == kRotNone) return;
   __syncwarp();  // the last token's have been read
   if (have) {
@@ -139,28 +145,34 @@ __device__ __forceinline__ void qk_angles(const QkArgs& p, const QkLane& l, bool
     for (int j = l.lane; j < p.F; j += D / 8) table[j] = angle(pos, freq[j]);
   }
   __syncwarp();
+  float2 a[4];
 #pragma unroll
-  for (int i = 0; i < 4; i++) turn[i] = l.angle >= 0 ? table[l.angle + i] : f2(1.f, 0.f);
+  for (int i = 0; i < 4; i++) a[i] = l.angle >= 0 ? table[l.angle + i] : f2(1.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    turn.c[i] = f2(a[2 * i].x, a[2 * i + 1].x);
+    turn.s[i] = f2(SIGN * a[2 * i].y, SIGN * a[2 * i + 1].y);
+    turn.m[i] = f2(-turn.s[i].x, -turn.s[i].y);
+  }
 }
 
-// Rotate a lane's channels (SIGN = -1: back).
-template <int ROT, int SIGN>
-__device__ __forceinline__ void rotate8(Eight& n, const QkLane& l, const float2 (&turn)[4]) {
+// Rotate a lane's channels.
+template <int ROT>
+__device__ __forceinline__ void rotate8(Eight& n, const QkLane& l, const Turn& turn) {
   if (ROT == kRotNone || l.angle < 0) return;
   if (ROT == kRotHalves) {
-    const float2 c[2] = {f2(turn[0].x, turn[1].x), f2(turn[2].x, turn[3].x)};
-    const float2 s[2] = {f2(SIGN * turn[0].y, SIGN * turn[1].y),
-                         f2(SIGN * turn[2].y, SIGN * turn[3].y)};
 #pragma unroll
     for (int i = 0; i < 2; i++) {
       const float2 u = n.v[i], v = n.v[2 + i];
-      n.v[i] = __ffma2_rn(f2(-v.x, -v.y), s[i], __fmul2_rn(u, c[i]));
-      n.v[2 + i] = __ffma2_rn(u, s[i], __fmul2_rn(v, c[i]));
+      n.v[i] = __ffma2_rn(v, turn.m[i], __fmul2_rn(u, turn.c[i]));
+      n.v[2 + i] = __ffma2_rn(u, turn.s[i], __fmul2_rn(v, turn.c[i]));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      const float u = n.v[i].x, v = n.v[i].y, c = turn[i].x, s = SIGN * turn[i].y;
+      const float u = n.v[i].x, v = n.v[i].y;
+      const float c = i & 1 ? turn.c[i / 2].y : turn.c[i / 2].x;
+      const float s = i & 1 ? turn.s[i / 2].y : turn.s[i / 2].x;
       n.v[i].x = __fmaf_rn(-v, s, __fmul_rn(u, c));
       n.v[i].y = __fmaf_rn(u, s, __fmul_rn(v, c));
     }
@@ -207,16 +219,21 @@ __device__ __forceinline__ QkUnit qk_unit(const QkSide& sd, int64_t u, int64_t e
 
 // Heads whose loads are under way together, and the blocks of a multiprocessor
 // that their registers are kept to.  10240 x (16 + 16) heads of 128, no
-// rotation: forward 28 us with 4 heads and 5 blocks (2 heads: 31), backward 57 us
+// rotation: forward 29 us with 4 heads and 5 blocks (2 heads: 31), backward 57 us
 // with 2 heads and 3 blocks (4 heads and 2 blocks: 64, 1 and 4: 68).  16384 x
-// (32 + 8) rotated with weights: forward 66 us (78 without the bound), backward
-// 113 us with 4 heads and 2 blocks (2 and 3: 119, 1 and 4: 131).
+// (32 + 8) rotated with weights: forward 61 us (78 without the bound), backward
+// 104 us with 4 heads and 2 blocks (2 and 3: 109, 1 and 4: 131); 8192 x (8 + 2)
+// heads of 256: 37 us with 2 and 3 (4 and 2: 53).
 constexpr int kQkForwardBatch = 4;
 __host__ __device__ constexpr int qk_forward_blocks(int rot, size_t element) {
   return rot == kRotNone ? 5 : element == 2 ? 4 : 3;
 }
-__host__ __device__ constexpr int qk_backward_batch(int rot) { return rot == kRotNone ? 2 : 4; }
-__host__ __device__ constexpr int qk_backward_blocks(int rot) { return rot == kRotNone ? 3 : 2; }
+__host__ __device__ constexpr int qk_backward_batch(int rot, int d) {
+  return rot == kRotNone || d == 256 ? 2 : 4;
+}
+__host__ __device__ constexpr int qk_backward_blocks(int rot, int d) {
+  return rot == kRotNone || d == 256 ? 3 : 2;
+}
 
 template <class IN, class OUT, int D, int ROT>
 __global__ void __launch_bounds__(kQkThreads, qk_forward_blocks(ROT, sizeof(IN)))
@@ -241,43 +258,60 @@ __global__ void __launch_bounds__(kQkThreads, qk_forward_blocks(ROT, sizeof(IN))
     const QkUnit u = qk_unit(sd, base + grp, end);
     const IN* x = static_cast<const IN*>(sd.x) + u.t * sd.ldx + (int64_t)u.h0 * D;
     OUT* y = static_cast<OUT*>(sd.out) + u.t * sd.ldout + (int64_t)u.h0 * D;
-    float2 turn[4];
-    Raw4 ra[kBatch] = {}, rb[kBatch] = {};
-    auto load = [&](int h) {
-#pragma unroll
-      for (int i = 0; i < kBatch; i++)
-        if (h + i < u.heads) {
-          ra[i] = *reinterpret_cast<const Raw4*>(x + (h + i) * D + l.a);
-          rb[i] = *reinterpret_cast<const Raw4*>(x + (h + i) * D + l.b);
-        }
-    };
-    load(0);  // under way while the angles are computed
-    qk_angles<D, ROT>(p, l, u.have, u.t, freq, table, turn);
-    // The warp's groups go through as many heads as the one with most.
-    for (int h = 0; h < sd.heads; h += kBatch) {
-      if (h > 0) load(h);
+    const IN *xa = x + l.a, *xb = x + l.b;
+    OUT *ya = y + l.a, *yb = y + l.b;
+    Turn turn;
+    Raw4 ra[kBatch], rb[kBatch];
+    // FULL: all of the batch's heads exist in all of the warp's groups, and
+    // their chains of operations can be interleaved.
+    auto load = [&](int left, bool full) {
 #pragma unroll
       for (int i = 0; i < kBatch; i++) {
-        if (h + i >= sd.heads) break;
-        Eight n;
-        widen4(ra[i], n.v);
-        widen4(rb[i], n.v + 2);
-        scale8(n, __frsqrt_rn(__fmaf_rn(dot8<D>(n, n), p.inv_m, p.eps)));
-        if (sd.w) times8(n, w);
-        rotate8<ROT, 1>(n, l, turn);
-        if (h + i < u.heads) {
-          store4(y + (h + i) * D + l.a, n.v);
-          store4(y + (h + i) * D + l.b, n.v + 2);
+        if (full || i < left) {
+          ra[i] = *reinterpret_cast<const Raw4*>(xa + i * D);
+          rb[i] = *reinterpret_cast<const Raw4*>(xb + i * D);
+        } else {
+          ra[i] = rb[i] = Raw4{};
         }
+      }
+    };
+    auto head = [&](int i, bool write) {
+      Eight n;
+      widen4(ra[i], n.v);
+      widen4(rb[i], n.v + 2);
+      scale8(n, rsqrtf(__fmaf_rn(dot8<D>(n, n), p.inv_m, p.eps)));
+      if (sd.w) times8(n, w);
+      rotate8<ROT>(n, l, turn);
+      if (write) {
+        store4(ya + i * D, n.v);
+        store4(yb + i * D, n.v + 2);
+      }
+    };
+    // The warp's groups go through as many heads as the one with most.
+    bool full = __all_sync(kFull, u.heads >= kBatch);
+    load(u.heads, full);  // under way while the angles are computed
+    qk_angles<D, ROT, 1>(p, l, u.have, u.t, freq, table, turn);
+    for (int h = 0; h < sd.heads; h += kBatch) {
+      if (full) {
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) head(i, true);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) head(i, h + i < u.heads);
+      }
+      xa += kBatch * D, xb += kBatch * D, ya += kBatch * D, yb += kBatch * D;
+      if (h + kBatch < sd.heads) {
+        full = __all_sync(kFull, u.heads >= h + 2 * kBatch);
+        load(u.heads - h - kBatch, full);
       }
     }
   }
 }
 
 template <class IN, class GR, int D, int ROT>
-__global__ void __launch_bounds__(kQkThreads, qk_backward_blocks(ROT))
+__global__ void __launch_bounds__(kQkThreads, qk_backward_blocks(ROT, D))
     k_qk_backward(const QkArgs p) {
-  constexpr int kLanes = D / 8, kGroups = kQkThreads / kLanes, kBatch = qk_backward_batch(ROT);
+  constexpr int kLanes = D / 8, kGroups = kQkThreads / kLanes, kBatch = qk_backward_batch(ROT, D);
   extern __shared__ uint64_t freq[];  // [F], and each group's [F] cosines and sines
   const bool isq = blockIdx.x < p.q.blocks;
   const QkSide& sd = isq ? p.q : p.k;
@@ -301,49 +335,67 @@ __global__ void __launch_bounds__(kQkThreads, qk_backward_blocks(ROT))
     const IN* x = static_cast<const IN*>(sd.x) + u.t * sd.ldx + (int64_t)u.h0 * D;
     const GR* dy = static_cast<const GR*>(sd.dy) + u.t * sd.lddy + (int64_t)u.h0 * D;
     IN* dx = static_cast<IN*>(sd.out) + u.t * sd.ldout + (int64_t)u.h0 * D;
-    float2 turn[4];
-    RawX xa[kBatch] = {}, xb[kBatch] = {};
-    RawG ga[kBatch] = {}, gb[kBatch] = {};
-    auto load = [&](int h) {
+    const IN *px = x + l.a, *qx = x + l.b;
+    const GR *pg = dy + l.a, *qg = dy + l.b;
+    IN *pd = dx + l.a, *qd = dx + l.b;
+    Turn turn;
+    RawX xa[kBatch], xb[kBatch];
+    RawG ga[kBatch], gb[kBatch];
+    auto load = [&](int left, bool full) {
 #pragma unroll
       for (int i = 0; i < kBatch; i++) {
-        const bool here = h + i < u.heads;
-        xa[i] = here ? *reinterpret_cast<const RawX*>(x + (h + i) * D + l.a) : RawX{};
-        xb[i] = here ? *reinterpret_cast<const RawX*>(x + (h + i) * D + l.b) : RawX{};
-        ga[i] = here ? *reinterpret_cast<const RawG*>(dy + (h + i) * D + l.a) : RawG{};
-        gb[i] = here ? *reinterpret_cast<const RawG*>(dy + (h + i) * D + l.b) : RawG{};
+        if (full || i < left) {
+          xa[i] = *reinterpret_cast<const RawX*>(px + i * D);
+          xb[i] = *reinterpret_cast<const RawX*>(qx + i * D);
+          ga[i] = *reinterpret_cast<const RawG*>(pg + i * D);
+          gb[i] = *reinterpret_cast<const RawG*>(qg + i * D);
+        } else {  // zeros: nothing for dw
+          xa[i] = xb[i] = RawX{};
+          ga[i] = gb[i] = RawG{};
+        }
       }
     };
-    load(0);
-    qk_angles<D, ROT>(p, l, u.have, u.t, freq, table, turn);
+    auto head = [&](int i, bool write) {
+      Eight n, e;  // the head and its gradient
+      widen4(xa[i], n.v);
+      widen4(xb[i], n.v + 2);
+      widen4(ga[i], e.v);
+      widen4(gb[i], e.v + 2);
+      rotate8<ROT>(e, l, turn);
+      const float r = rsqrtf(__fmaf_rn(dot8<D>(n, n), p.inv_m, p.eps));
+      if (sd.w) {
+        const float2 rr = f2(r, r);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          dw.v[j] = __ffma2_rn(e.v[j], __fmul2_rn(n.v[j], rr), dw.v[j]);
+        times8(e, w);
+      }
+      const float m = __fmul_rn(dot8<D>(n, e), p.inv_m);
+      const float z = -__fmul_rn(__fmul_rn(r, r), m);
+#pragma unroll
+      for (int j = 0; j < 4; j++) e.v[j] = __ffma2_rn(n.v[j], f2(z, z), e.v[j]);
+      scale8(e, r);
+      if (write) {
+        store4(pd + i * D, e.v);
+        store4(qd + i * D, e.v + 2);
+      }
+    };
+    bool full = __all_sync(kFull, u.heads >= kBatch);
+    load(u.heads, full);
+    qk_angles<D, ROT, -1>(p, l, u.have, u.t, freq, table, turn);
     for (int h = 0; h < sd.heads; h += kBatch) {
-      if (h > 0) load(h);
+      if (full) {
 #pragma unroll
-      for (int i = 0; i < kBatch; i++) {
-        if (h + i >= sd.heads) break;
-        Eight n, e;  // the head and its gradient (zeros for a group without one)
-        widen4(xa[i], n.v);
-        widen4(xb[i], n.v + 2);
-        widen4(ga[i], e.v);
-        widen4(gb[i], e.v + 2);
-        rotate8<ROT, -1>(e, l, turn);
-        const float r = __frsqrt_rn(__fmaf_rn(dot8<D>(n, n), p.inv_m, p.eps));
-        if (sd.w) {
-          const float2 rr = f2(r, r);
+        for (int i = 0; i < kBatch; i++) head(i, true);
+      } else {
 #pragma unroll
-          for (int j = 0; j < 4; j++)
-            dw.v[j] = __ffma2_rn(e.v[j], __fmul2_rn(n.v[j], rr), dw.v[j]);
-          times8(e, w);
-        }
-        const float m = __fmul_rn(dot8<D>(n, e), p.inv_m);
-        const float z = -__fmul_rn(__fmul_rn(r, r), m);
-#pragma unroll
-        for (int j = 0; j < 4; j++) e.v[j] = __ffma2_rn(n.v[j], f2(z, z), e.v[j]);
-        scale8(e, r);
-        if (h + i < u.heads) {
-          store4(dx + (h + i) * D + l.a, e.v);
-          store4(dx + (h + i) * D + l.b, e.v + 2);
-        }
+        for (int i = 0; i < kBatch; i++) head(i, h + i < u.heads);
+      }
+      px += kBatch * D, qx += kBatch * D, pg += kBatch * D, qg += kBatch * D;
+      pd += kBatch * D, qd += kBatch * D;
+      if (h + kBatch < sd.heads) {
+        full = __all_sync(kFull, u.heads >= h + 2 * kBatch);
+        load(u.heads - h - kBatch, full);
       }
     }
   }
@@ -369,6 +421,7 @@ __global__ void __launch_bounds__(1024)
   __shared__ float red[32][32];
   float* out = blockIdx.y == 0 ? d_wq : d_wk;
   if (!out) return;
+  pdl_wait();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
   const int blocks = blockIdx.y == 0 ? q_blocks : k_blocks;
   const float* col = partial + (blockIdx.y == 0 ? 0 : (int64_t)q_blocks * D) + c;
@@ -395,7 +448,7 @@ __global__ void __launch_bounds__(1024)
 constexpr int kQkUnitHeads = 32;
 constexpr int kQkFill = 148 * 4 * 8;
 
-static int qk_sums(int rot) { return 148 * qk_backward_blocks(rot); }
+static int qk_sums(int rot, int d) { return 148 * qk_backward_blocks(rot, d); }
 
 static bool qk_plan(QkArgs& p, int64_t T, int Hq, int Hk, int d, int sums) {
   p.T = T;
@@ -541,7 +594,7 @@ extern "C" size_t gdn_qk_norm_backward_workspace_bytes(int64_t T, int Hq, int Hk
   if (check_shape(T, Hq, Hk, d) != GDN_OK || T == 0) return 0;
   gdn::QkArgs p{};
   // (the plan with more sums; a rotation's backward keeps fewer)
-  if (!gdn::qk_plan(p, T, Hq, Hk, d, gdn::qk_sums(gdn::kRotNone))) return 0;
+  if (!gdn::qk_plan(p, T, Hq, Hk, d, gdn::qk_sums(gdn::kRotNone, d))) return 0;
   return (size_t)(p.q.blocks + p.k.blocks) * d * sizeof(float);
 }
 
@@ -579,7 +632,7 @@ extern "C" int gdn_qk_norm_backward(const void* q, int64_t ldq, const void* k, i
     if (!aligned(workspace, 16)) return GDN_ERR_INVALID_ARG;
   }
   gdn::QkArgs p{};
-  if (!gdn::qk_plan(p, T, Hq, Hk, d, weights ? gdn::qk_sums(rot_kind(rot_dim, interleaved)) : 0)) return GDN_ERR_UNSUPPORTED;
+  if (!gdn::qk_plan(p, T, Hq, Hk, d, weights ? gdn::qk_sums(rot_kind(rot_dim, interleaved), d) : 0)) return GDN_ERR_UNSUPPORTED;
   p.q.x = q, p.q.ldx = ldq, p.q.w = wq, p.q.dy = d_oq, p.q.lddy = lddoq, p.q.out = d_q;
   p.q.ldout = lddq;
   p.k.x = k, p.k.ldx = ldk, p.k.w = wk, p.k.dy = d_ok, p.k.lddy = lddok, p.k.out = d_k;
@@ -594,9 +647,10 @@ extern "C" int gdn_qk_norm_backward(const void* q, int64_t ldq, const void* k, i
                     rot_kind(rot_dim, interleaved), st) != cudaSuccess)
     return GDN_ERR_CUDA;
   if (weights) {
-    gdn::k_qk_weight_sum<<<dim3((unsigned)(d / 32), 2), 1024, 0, st>>>(
-        p.partial, (int)p.q.blocks, (int)p.k.blocks, d, d_wq, d_wk);
-    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    if (gdn::launch_dependent(gdn::k_qk_weight_sum, dim3((unsigned)(d / 32), 2), dim3(1024), 0,
+                              st, (const float*)p.partial, (int)p.q.blocks, (int)p.k.blocks, d,
+                              d_wq, d_wk) != cudaSuccess)
+      return GDN_ERR_CUDA;
   }
   return GDN_OK;
 }
