@@ -25,9 +25,9 @@
  * Conventions are those of gdn_cpr.h (device pointers of the current device,
  * caller-owned memory, argument errors before any launch, device error word,
  * no float atomics) with these differences: x, g, h and their gradients
- * [tokens, D] may have a row stride (ld*, in elements, >= D) and need only
- * the alignment of their elements; fp32 arrays [rows, D] are contiguous and
- * 16-byte aligned.  g may be -inf (a = 0); it must not be NaN or +inf.
+ * [tokens, D] may have a row stride (ld*, in elements, >= D); they and the
+ * contiguous fp32 arrays [rows, D] need only the alignment of their elements
+ * (16 bytes for a decode state).  Rows that start on 16 bytes are the fast ones.  g may be -inf (a = 0); it must not be NaN or +inf.
  * D is any size from 1 to 2^24, total_tokens up to 2^31 - 4097, strides up to
  * 2^27 elements.
  */

@@ -857,14 +857,191 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(false))
   }
 }
 
-// One block per row (a row's pos is read and written by one block).
+// Short sequences: a thread takes one channel of a whole sequence, chunk by
+// chunk, with the operations of the kernels above in the same order.  There is
+// no tile, no hand-over and no ring to set up, which is most of what a block
+// spends on a sequence of a few tokens.
+constexpr int kGlrShortThreads = 128;
+
+template <class IN, class G, class OUT, int MODE>
+__global__ void __launch_bounds__(kGlrShortThreads) k_glr_short_forward(const GlrArgs p) {
+  const int n = blockIdx.x / p.slabs, ch = blockIdx.x % p.slabs * kGlrShortThreads + threadIdx.x;
+  glr_report(p);
+  int start, L;
+  if (!glr_seq(p, n, start, L)) return;
+  const bool live = ch < p.D;
+  const IN* x = static_cast<const IN*>(p.x) + (int64_t)start * p.ldx + ch;
+  const G* g = static_cast<const G*>(p.g) + (int64_t)start * p.ldg + ch;
+  OUT* h = static_cast<OUT*>(p.h) + (int64_t)start * p.ldh + ch;
+  float H[1], hv[1], A = 1.f, B = 0.f;
+  row_get<1>(p.h0, n, p.D, ch, H);
+  hv[0] = H[0];
+  float Hm = H[0];
+  GlrSource<IN, 1, false> sx;
+  GlrSource<G, 1, false> sg;
+  auto load = [&](int t) {
+    const int have = live && t < L ? min(kGlrChunk, L - t) : 0;
+    sx.load(x + (int64_t)t * p.ldx, p.ldx, have);
+    sg.load(g + (int64_t)t * p.ldg, p.ldg, have);
+  };
+  load(0);
+  for (int t0 = 0; live && t0 < L; t0 += kGlrChunk) {
+    sx.take();
+    sg.take();
+    load(t0 + kGlrChunk);
+    if (p.carry && t0 % kGlrTile == 0)
+      p.carry[(int64_t)(start / kGlrTile + n + t0 / kGlrTile) * p.D + ch] = H[0];
+    Hm = H[0];
+    const int have = min(kGlrChunk, L - t0);
+    OUT* out = h + (int64_t)t0 * p.ldh;
+#pragma unroll
+    for (int t = 0; t < kGlrChunk; t++) {
+      float xv[1], gv[1];
+      widen(sx.get(t), xv);
+      widen(sg.get(t), gv);
+      unsigned far = 0;
+      const float k = gate_of<MODE>(gv[0], far, 0), a = gate_a<MODE>(k, far, 0);
+      const float b = gate_b<MODE>(k, far, 0, xv[0]);
+      A = t ? __fmul_rn(a, A) : a;
+      B = t ? __fmaf_rn(a, B, b) : __fmaf_rn(a, 0.f, b);
+      hv[0] = __fmaf_rn(A, Hm, B);
+      if (t < have) put(row_at(out, p.ldh, t), hv);
+    }
+    H[0] = hv[0];
+  }
+  if (p.s_final && live) put(p.s_final + (int64_t)n * p.D + ch, hv);
+  if (p.st.h) {
+    const int slot = glr_slot_block(p.slot_idx, n, p.st.n_slots);
+    const int pos = L % kGlrChunk;
+    if (slot < 0) {
+      if (threadIdx.x == 0) atomicOr(p.st.error, kErrPos);
+      return;
+    }
+    if (ch == 0) p.st.pos[slot] = pos;
+    if (live) {
+      const int64_t to = (int64_t)slot * p.D + ch;
+      p.st.h[to] = pos ? Hm : hv[0];
+      p.st.a[to] = pos ? A : 1.f;
+      p.st.b[to] = pos ? B : 0.f;
+    }
+  }
+}
+
+template <class IN, class G, class OUT, int MODE>
+__global__ void __launch_bounds__(kGlrShortThreads) k_glr_short_backward(const GlrArgs p) {
+  __shared__ float enter[kGlrChunks][kGlrShortThreads];  // a thread's own column
+  const int n = blockIdx.x / p.slabs, ch = blockIdx.x % p.slabs * kGlrShortThreads + threadIdx.x;
+  glr_report(p);
+  int start, L;
+  if (!glr_seq(p, n, start, L)) return;
+  if (ch >= p.D) return;
+  const IN* x = static_cast<const IN*>(p.x) + (int64_t)start * p.ldx + ch;
+  const G* g = static_cast<const G*>(p.g) + (int64_t)start * p.ldg + ch;
+  const OUT* dh = static_cast<const OUT*>(p.d_h) + (int64_t)start * p.lddh + ch;
+  IN* dx = static_cast<IN*>(p.d_x) + (int64_t)start * p.lddx + ch;
+  G* dg = static_cast<G*>(p.d_g) + (int64_t)start * p.lddg + ch;
+  float mu[1];
+  row_get<1>(p.ds_final, n, p.D, ch, mu);
+  float w[kGlrChunk], A[kGlrChunk], B[kGlrChunk];
+  unsigned far;
+  GlrSource<IN, 1, false> sx;
+  GlrSource<G, 1, false> sg;
+  GlrSource<OUT, 1, false> sd;
+  auto fold = [&](int t0, int have) {  // the chunk's gates and maps
+    sx.load(x + (int64_t)t0 * p.ldx, p.ldx, have);
+    sg.load(g + (int64_t)t0 * p.ldg, p.ldg, have);
+    sx.take();
+    sg.take();
+    far = 0;
+#pragma unroll
+    for (int t = 0; t < kGlrChunk; t++) {
+      float xv[1], gv[1];
+      widen(sx.get(t), xv);
+      widen(sg.get(t), gv);
+      w[t] = gate_of<MODE>(gv[0], far, t);
+      const float a = gate_a<MODE>(w[t], far, t);
+      const float b = gate_b<MODE>(w[t], far, t, xv[0]);
+      A[t] = t ? __fmul_rn(a, A[t - 1]) : a;
+      B[t] = t ? __fmaf_rn(a, B[t - 1], b) : __fmaf_rn(a, 0.f, b);
+    }
+  };
+  for (int tile = (L - 1) / kGlrTile; L > 0 && tile >= 0; tile--) {
+    const int first = tile * kGlrTile;
+    const int chunks = min(kGlrChunks, (L - first + kGlrChunk - 1) / kGlrChunk);
+    // The states that enter the tile's chunks, from its carry row.
+    float H = p.carry[(int64_t)(start / kGlrTile + n + tile) * p.D + ch];
+    enter[0][threadIdx.x] = H;
+#pragma unroll 1
+    for (int c = 1; c < chunks; c++) {
+      fold(first + (c - 1) * kGlrChunk, kGlrChunk);
+      H = __fmaf_rn(A[kGlrChunk - 1], H, B[kGlrChunk - 1]);
+      enter[c][threadIdx.x] = H;
+    }
+#pragma unroll 1
+    for (int c = chunks - 1; c >= 0; c--) {
+      const float Hm = enter[c][threadIdx.x];
+      const int t0 = first + c * kGlrChunk, have = min(kGlrChunk, L - t0);
+      sd.load(dh + (int64_t)t0 * p.lddh, p.lddh, have);
+      sd.take();
+      fold(t0, have);
+      IN* ox = dx + (int64_t)t0 * p.lddx;
+      G* og = dg + (int64_t)t0 * p.lddg;
+      float M = 0.f, mm = mu[0];
+#pragma unroll
+      for (int t = 0; t < kGlrChunk; t++) {
+        float dv[1];
+        widen(sd.get(t), dv);
+        M = t ? __fmaf_rn(A[t], dv[0], M) : __fmul_rn(A[0], dv[0]);
+      }
+#pragma unroll
+      for (int t = kGlrChunk - 1; t >= 0; t--) {
+        float dv[1], xv[1], fx[1], fg[1];
+        widen(sd.get(t), dv);
+        widen(sx.get(t), xv);
+        const float before = t ? __fmaf_rn(A[t ? t - 1 : 0], Hm, B[t ? t - 1 : 0]) : Hm;
+        const float lam = __fadd_rn(dv[0], mm);
+        mm = __fmul_rn(gate_a<MODE>(w[t], far, t), lam);
+        fx[0] = gate_b<MODE>(w[t], far, t, lam);
+        fg[0] = __fmul_rn(mm, MODE == GDN_GLR_INPUT_COMPLEMENT ? __fsub_rn(before, xv[0])
+                                                               : before);
+        if (t < have) {
+          put(row_at(ox, p.lddx, t), fx);
+          put(row_at(og, p.lddg, t), fg);
+        }
+      }
+      mu[0] = __fmaf_rn(A[kGlrChunk - 1], mu[0], M);
+    }
+  }
+  if (p.d_h0) put(p.d_h0 + (int64_t)n * p.D + ch, mu);
+}
+
+// One block per row (a row's pos is read and written by one block).  A row's
+// first channels are loaded beside its pos, not behind it.
 constexpr int kGlrStepThreads = 1024;
 
 template <class IN, class G, class OUT, int V, int MODE>
 __global__ void __launch_bounds__(kGlrStepThreads) k_glr_step(const GlrArgs p) {
   const int b = blockIdx.x;
   const int slot = glr_slot_block(p.slot_idx, b, p.st.n_slots);
-  const int pos = slot < 0 ? -1 : p.st.pos[slot];
+  if (slot < 0) {
+    if (threadIdx.x == 0) atomicOr(p.st.error, kErrPos);
+    return;
+  }
+  const IN* x = static_cast<const IN*>(p.x) + (int64_t)b * p.ldx;
+  const G* g = static_cast<const G*>(p.g) + (int64_t)b * p.ldg;
+  OUT* h = static_cast<OUT*>(p.h) + (int64_t)b * p.ldh;
+  const int64_t base = (int64_t)slot * p.D;
+  float xv[V], gv[V], H[V], A[V], B[V];
+  auto load = [&](int ch) {
+    if (ch >= p.D) return;
+    widen(raw_load<IN, V>(x + ch), xv);
+    widen(raw_load<G, V>(g + ch), gv);
+    widen(raw_load<float, V>(p.st.h + base + ch), H);
+    widen(raw_load<float, V>(p.st.a + base + ch), A);
+    widen(raw_load<float, V>(p.st.b + base + ch), B);
+  };
+  load(threadIdx.x * V);
+  const int pos = p.st.pos[slot];
   if (pos < 0 || pos >= kGlrChunk) {
     if (threadIdx.x == 0) atomicOr(p.st.error, kErrPos);
     return;
@@ -872,17 +1049,8 @@ __global__ void __launch_bounds__(kGlrStepThreads) k_glr_step(const GlrArgs p) {
   __syncthreads();  // every thread has read pos
   const bool full = pos == kGlrChunk - 1;
   if (threadIdx.x == 0) p.st.pos[slot] = full ? 0 : pos + 1;
-  const IN* x = static_cast<const IN*>(p.x) + (int64_t)b * p.ldx;
-  const G* g = static_cast<const G*>(p.g) + (int64_t)b * p.ldg;
-  OUT* h = static_cast<OUT*>(p.h) + (int64_t)b * p.ldh;
-  const int64_t base = (int64_t)slot * p.D;
-  for (int ch = threadIdx.x * V; ch < p.D; ch += kGlrStepThreads * V) {
-    float xv[V], gv[V], H[V], A[V], B[V], hv[V];
-    widen(raw_load<IN, V>(x + ch), xv);
-    widen(raw_load<G, V>(g + ch), gv);
-    widen(raw_load<float, V>(p.st.h + base + ch), H);
-    widen(raw_load<float, V>(p.st.a + base + ch), A);
-    widen(raw_load<float, V>(p.st.b + base + ch), B);
+  for (int ch = threadIdx.x * V; ch < p.D; ch += blockDim.x * V) {
+    float hv[V];
 #pragma unroll
     for (int v = 0; v < V; v++) {
       unsigned far = 0;
@@ -899,7 +1067,14 @@ __global__ void __launch_bounds__(kGlrStepThreads) k_glr_step(const GlrArgs p) {
     if (full) put(p.st.h + base + ch, hv);
     put(p.st.a + base + ch, A);
     put(p.st.b + base + ch, B);
+    load(ch + blockDim.x * V);
   }
+}
+
+template <int V>
+static unsigned glr_step_threads(int D) {
+  const int n = (D / V + 31) / 32 * 32;
+  return (unsigned)(n < 32 ? 32 : n > kGlrStepThreads ? kGlrStepThreads : n);
 }
 
 // ----------------------------------------------------------------------------
@@ -998,9 +1173,21 @@ static cudaError_t glr_launch(GlrOp op, GlrArgs& p, bool pairs, cudaStream_t st)
   p.slabs = (p.D + kGlrSlab - 1) / kGlrSlab;
   if (op == kGlrStep) {
     if (pairs)
-      k_glr_step<IN, G, OUT, 2, MODE><<<(unsigned)p.N, kGlrStepThreads, 0, st>>>(p);
+      k_glr_step<IN, G, OUT, 2, MODE><<<(unsigned)p.N, glr_step_threads<2>(p.D), 0, st>>>(p);
     else
-      k_glr_step<IN, G, OUT, 1, MODE><<<(unsigned)p.N, kGlrStepThreads, 0, st>>>(p);
+      k_glr_step<IN, G, OUT, 1, MODE><<<(unsigned)p.N, glr_step_threads<1>(p.D), 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  // Sequences of up to 64 tokens on average, and more of them than one wave of
+  // tile blocks takes: 64 sequences of 4096 channels, forward and backward, 300
+  // tokens: 35 us (tiles: 130), 4096: 127 (161), 8192: 238 (207).
+  if (p.T <= (int64_t)64 * p.N && (int64_t)p.N * p.slabs > 3 * 148) {
+    p.slabs = (p.D + kGlrShortThreads - 1) / kGlrShortThreads;
+    const unsigned blocks = (unsigned)p.N * (unsigned)p.slabs;
+    if (op == kGlrFwd)
+      k_glr_short_forward<IN, G, OUT, MODE><<<blocks, kGlrShortThreads, 0, st>>>(p);
+    else
+      k_glr_short_backward<IN, G, OUT, MODE><<<blocks, kGlrShortThreads, 0, st>>>(p);
     return cudaGetLastError();
   }
   GlrBoxes box{};
@@ -1118,8 +1305,9 @@ extern "C" int gdn_glr_forward(const void* x, int64_t ldx, int in_dtype, const v
     pairs = pairs && paired(x, ldx, in_dtype) && paired(g, ldg, g_dtype) &&
             paired(h, ldh, out_dtype);
   }
-  if (!aligned(h0, 16) || !aligned(s_final, 16) || !aligned(carry, 16) || !aligned(slot_idx, 4))
+  if (!aligned(h0, 4) || !aligned(s_final, 4) || !aligned(carry, 4) || !aligned(slot_idx, 4))
     return GDN_ERR_INVALID_ARG;
+  pairs = pairs && aligned(s_final, 8);  // (the others are read or written one at a time)
   if (slot_idx && !state) return GDN_ERR_INVALID_ARG;
   if (state) {
     if ((rc = check_state(*state)) != GDN_OK) return rc;
@@ -1174,7 +1362,7 @@ extern "C" int gdn_glr_backward(const void* x, int64_t ldx, int in_dtype, const 
             paired(d_h, lddh, dh_dtype) && paired(d_x, lddx, in_dtype) &&
             paired(d_g, lddg, g_dtype);
   }
-  if (!aligned(carry, 16) || !aligned(ds_final, 16) || !aligned(d_h0, 16))
+  if (!aligned(carry, 4) || !aligned(ds_final, 4) || !aligned(d_h0, 4))
     return GDN_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (n_seqs == 0)

@@ -239,7 +239,7 @@ BAD_BATCH = [
 
 @pytest.mark.parametrize("over,expect", BAD_BATCH + [
     (dict(odt=2), BAD), (dict(h=None), BAD), (dict(h=ODD), BAD), (dict(ldh=64), BAD),
-    (dict(h0=FAKE + 4), BAD), (dict(sf=FAKE + 8), BAD), (dict(carry=FAKE + 4), BAD),
+    (dict(h0=ODD), BAD), (dict(sf=FAKE + 2), BAD), (dict(carry=ODD), BAD),
     (dict(slot=FAKE), BAD), (dict(st=glr_state(n_slots=1)), BAD),
     (dict(st=glr_state(n_slots=0)), BAD), (dict(st=glr_state(h=None)), BAD),
     (dict(st=glr_state(pos=None)), BAD), (dict(st=glr_state(a=FAKE + 4)), BAD),
@@ -258,10 +258,10 @@ def glr_bwd(**over):
 
 
 @pytest.mark.parametrize("over,expect", BAD_BATCH + [
-    (dict(carry=None), BAD), (dict(carry=FAKE + 4), BAD), (dict(dh=None), BAD),
+    (dict(carry=None), BAD), (dict(carry=FAKE + 2), BAD), (dict(dh=None), BAD),
     (dict(ddt=9), BAD), (dict(lddh=64), BAD), (dict(dx=None), BAD), (dict(dx=ODD), BAD),
-    (dict(lddx=99), BAD), (dict(dg=None), BAD), (dict(lddg=99), BAD), (dict(ds=FAKE + 4), BAD),
-    (dict(dh0=FAKE + 4), BAD),
+    (dict(lddx=99), BAD), (dict(dg=None), BAD), (dict(lddg=99), BAD), (dict(ds=FAKE + 2), BAD),
+    (dict(dh0=ODD), BAD),
 ])
 def test_glr_backward_refuses(over, expect):
     assert glr_bwd(**over) == expect

@@ -393,3 +393,80 @@ def test_binding_refuses(gdn):
         gdn.glr_forward(x, g, cu, h=torch.empty((1, 16), dtype=BF, device="cuda").expand(8, 16))
     with pytest.raises(ValueError, match="state"):
         gdn.glr_decode_step(gdn.GlrDecodeState(8, 15), x, g)
+
+
+SHAPES = {  # (lengths, channels): the launch shapes that sizes choose between
+    "short": ([3, 0, 17, 64, 1, 130, 40, 16] * 8, 512),        # many short sequences
+    "short, one long": ([2] * 60 + [900], 513),
+    "tiles": ([300, 5, 700, 129] * 4, 512),                    # a block for each slab
+    "clusters of 8": ([5000], 64),
+    "clusters of 4": ([3000, 1, 2000], 512),
+    "two for uneven": ([1500, 10, 300, 0, 700], 2048),
+    "last step partly empty": ([129], 32),
+    "rows off 16 bytes": ([700, 300], 1027),
+}
+
+
+@pytest.mark.parametrize("name", list(SHAPES))
+@pytest.mark.parametrize("complement", [False, True])
+def test_every_launch_shape_has_the_same_bits(gdn, name, complement):
+    """Each sequence of the batch alone, and its first 32 and last odd channels
+    alone, go through other kernels, clusters and stages: the bits are the same."""
+    lens, D = SHAPES[name]
+    x, g, dh, h0, ds, cu = draw(lens, D, 61)
+    edges = cu.tolist()
+
+    def both(rows, cols, n):
+        c = W.cu_seqlens_of([lens[i] for i in n], "cuda")
+        take = lambda t: t[rows][:, cols].contiguous()  # noqa: E731
+        per = lambda t: t[n][:, cols].contiguous()      # noqa: E731
+        a = (take(x), take(g), c)
+        h, fin, carry, err = gdn.glr_forward(*a, h0=per(h0), complement=complement,
+                                             want_carry=True)
+        ok(gdn, err)
+        grads, err = gdn.glr_backward(*a, carry, take(dh), ds_final=per(ds),
+                                      complement=complement)
+        ok(gdn, err)
+        return (h, grads["dx"], grads["dg"]), (fin, grads["dh0"])
+
+    everything = list(range(len(lens)))
+    tok, seq = both(slice(None), slice(None), everything)
+    for n in sorted({0, len(lens) // 2, len(lens) - 1}):
+        rows = slice(edges[n], edges[n + 1])
+        for cols in (slice(None), slice(0, 32), slice(D - 7, D)):
+            t1, s1 = both(rows, cols, [n])
+            assert all(torch.equal(a, b[rows][:, cols]) for a, b in zip(t1, tok)), (n, cols)
+            assert all(torch.equal(a[0], b[n][cols]) for a, b in zip(s1, seq)), (n, cols)
+    # and the oracle, on a few channels
+    ch = [0, D // 2, D - 1]
+    args = (f64(x[:, ch]), f64(g[:, ch]), lens)
+    want, _ = glr.forward(*args, f64(h0[:, ch]), complement)
+    bound, _ = glr.forward_bound(*args, f64(h0[:, ch]), complement)
+    close(tok[0][:, ch], want, bound + 2.0 ** -8 * (np.abs(want) + bound))
+    wx, wg, w0 = glr.backward(*args, f64(dh[:, ch]), f64(h0[:, ch]), f64(ds[:, ch]), complement)
+    bx, bg, b0 = glr.backward_bound(*args, f64(dh[:, ch]), f64(h0[:, ch]), f64(ds[:, ch]),
+                                    complement)
+    close(tok[2][:, ch], wg, bg, "dg")
+    close(seq[1][:, ch], w0, b0, "dh0")
+
+
+def test_decode_states_from_short_sequences(gdn):
+    """The short kernel's final states: slots, positions and a twice-named slot."""
+    lens, D = [3, 0, 17, 64, 1, 33, 40, 16] * 8, 512
+    x, g, _, h0, _, cu = draw(lens, D, 62)
+    idx = torch.randperm(64, generator=torch.Generator().manual_seed(1)).to(torch.int32)
+    idx[9] = idx[4]
+    state = gdn.GlrDecodeState(64, D)
+    _, fin, _, err = gdn.glr_forward(x, g, cu, h0=h0, state=state, slot_idx=idx.cuda())
+    ok(gdn, err)
+    assert gdn.check_error(state.error) & gdn.GDN_DEVERR_POS
+    value = torch.where((state.pos > 0)[:, None], state.a * state.h + state.b, state.h)
+    keep = [n for n in range(64) if n != 9]
+    slots = idx[keep].long()
+    assert state.pos[slots].tolist() == [lens[n] % 16 for n in keep]
+    assert torch.allclose(value[slots], fin[keep], rtol=1e-6, atol=1e-6)
+    one = gdn.GlrDecodeState(64, D)     # a sequence alone takes the tile kernel
+    edges = cu.tolist()
+    rows = slice(edges[2], edges[3])
+    gdn.glr_forward(x[rows], g[rows], W.cu_seqlens_of([lens[2]], "cuda"), h0=h0[2:3], state=one)
+    assert all(torch.equal(a[0], b[int(idx[2])]) for a, b in zip(one.tensors(), state.tensors()))
