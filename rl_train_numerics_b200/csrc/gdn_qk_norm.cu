@@ -145,9 +145,11 @@ __device__ __forceinline__ void qk_angles(const QkArgs& p, const QkLane& l, bool
     for (int j = l.lane; j < p.F; j += D / 8) table[j] = angle(pos, freq[j]);
   }
   __syncwarp();
+  // A group without a token has no table: it must not turn its zeros by what an
+  // earlier kernel left there.
   float2 a[4];
 #pragma unroll
-  for (int i = 0; i < 4; i++) a[i] = l.angle >= 0 ? table[l.angle + i] : f2(1.f, 0.f);
+  for (int i = 0; i < 4; i++) a[i] = have && l.angle >= 0 ? table[l.angle + i] : f2(1.f, 0.f);
 #pragma unroll
   for (int i = 0; i < 2; i++) {
     turn.c[i] = f2(a[2 * i].x, a[2 * i + 1].x);

@@ -207,3 +207,20 @@ def test_binding_refuses(gdn):
         gdn.qk_norm_forward(q[..., :32].contiguous(), None)
     with pytest.raises(gdn.GdnError, match="UNSUPPORTED"):
         gdn.qk_norm_forward(q, k, positions=kw["positions"], inv_freq=kw["inv_freq"][:5])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_idle_groups_add_nothing_to_the_weights(gdn, interleaved):
+    """Lane groups without a token must not read what an earlier kernel left in
+    shared memory: here a run over NaNs, which fills it on every multiprocessor."""
+    nan = torch.full((2048, 2048), float("nan"), device="cuda")
+    cu = torch.tensor([0, 1000, 2048], dtype=torch.int32, device="cuda")
+    q, k, dq, dk, kw = draw(37, 5, 1, 128, 78, rot=64)
+    for rot in (16, 64):
+        kw["inv_freq"] = kw["inv_freq"][:rot // 2].contiguous()
+        gdn.glr_forward(nan, nan, cu)
+        grads = gdn.qk_norm_backward(q, k, dq, dk, norm="rms", interleaved=interleaved, **kw)
+        for (x, dy, rest), s in zip(sides(q, k, dq, dk, kw), "qk"):
+            opts = dict(norm="rms", interleaved=interleaved)
+            close(grads["dw" + s], qk_norm.backward(x, dy, *rest, **opts)[1],
+                  qk_norm.backward_bound(x, dy, *rest, **opts)[1])
