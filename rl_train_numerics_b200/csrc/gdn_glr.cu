@@ -1094,6 +1094,8 @@ enum GlrOp { kGlrFwd, kGlrBwd, kGlrStep };
 // x 1000 in 9 sequences: 84 against 72 us); where blocks are many the others
 // cover that, and three blocks with two stages win (16384 x 2048 in 32: 90
 // against 107 us).
+constexpr size_t kGlrStatic = 4608;  // shared memory of a block that its launch does not size
+
 struct GlrShape {
   int cs, stages;
   size_t smem;
@@ -1101,7 +1103,7 @@ struct GlrShape {
 
 static GlrShape glr_shape(const GlrArgs& p, size_t stage, int most, bool backward) {
   constexpr int64_t kSms = 148;
-  constexpr size_t kSmem = 228 * 1024, kBlock = 1024 + 4608;  // of an SM; fixed per block
+  constexpr size_t kSmem = 228 * 1024, kBlock = 1024 + kGlrStatic;  // of an SM; fixed per block
   auto maps = [](int cs) { return (size_t)2 * cs * kGlrChunks * kGlrSlab * sizeof(float2) + 128; };
   auto places = [&](int cs) {
     const int64_t n = kSmem / (kBlock + maps(cs) + 2 * stage);
@@ -1135,8 +1137,9 @@ static cudaError_t glr_run(K kernel, int threads, size_t stage, int most, bool b
                            GlrArgs& p, const GlrBoxes& box, cudaStream_t st) {
   const GlrShape sh = glr_shape(p, stage, most, backward);
   p.stages = sh.stages;
+  // The kernel's limit, not this call's size: two host threads may be here at once.
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sh.smem);
+                                       227 * 1024 - (int)kGlrStatic);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;

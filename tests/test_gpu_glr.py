@@ -470,3 +470,36 @@ def test_decode_states_from_short_sequences(gdn):
     rows = slice(edges[2], edges[3])
     gdn.glr_forward(x[rows], g[rows], W.cu_seqlens_of([lens[2]], "cuda"), h0=h0[2:3], state=one)
     assert all(torch.equal(a[0], b[int(idx[2])]) for a, b in zip(one.tensors(), state.tensors()))
+
+
+def test_two_threads_with_different_shapes(gdn):
+    """Calls of one kernel with different launch shapes, at once from two host threads."""
+    import threading
+    jobs = []
+    for lens, D in (([5000], 64), ([700] * 40, 512), ([129, 300], 2048)):
+        x, g, dh, h0, ds, cu = draw(lens, D, 70)
+
+        def job(x=x, g=g, dh=dh, h0=h0, ds=ds, cu=cu):
+            h, fin, carry, err = gdn.glr_forward(x, g, cu, h0=h0, want_carry=True)
+            grads, err2 = gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds)
+            return h, fin, grads["dx"], grads["dg"], grads["dh0"], err, err2
+        jobs.append((job, [t.clone() for t in job()]))
+    torch.cuda.synchronize()
+    failed = []
+
+    def loop(job, want, stream):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(200):
+                    got = job()
+                stream.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                failed.append("other bits")
+        except Exception as e:  # a refused launch
+            failed.append(e)
+    threads = [threading.Thread(target=loop, args=(*j, torch.cuda.Stream())) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
