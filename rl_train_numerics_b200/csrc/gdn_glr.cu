@@ -13,8 +13,8 @@
 // decode step, which keeps (H, A, B), has the forward's bits.  Every channel's
 // operations are those of its own sequence in order, so nothing depends on
 // the batch, on V or on how tiles are spread over blocks.  Tokens behind a
-// sequence's end are identity steps (a = 1, b = 0), which leave A, B and H as
-// they are.
+// sequence's end are identity steps (a = 1, b = -0), which leave A, B and H as
+// they are, the sign of a zero included.
 //
 // Few sequences of few channels would leave most of the device idle: then a
 // cluster of 2, 4 or 8 blocks takes as many neighbouring tiles at a time, every
@@ -51,7 +51,7 @@ template <int V>
 constexpr int kGlrBlock = kGlrThreads<V> + 32;  // and the service warp
 static_assert(kGlrTile == GDN_GLR_TILE, "carry rows are tile starts");
 
-// V consecutive elements as loaded, all-zero bits for masked ones.
+// V consecutive elements as loaded, zeros for masked ones.
 template <class T, int V>
 struct Raw;
 template <>
@@ -71,10 +71,12 @@ struct Raw<float, 2> {
   using type = float2;
 };
 
-__device__ __forceinline__ void raw_zero(unsigned short& r) { r = 0; }
-__device__ __forceinline__ void raw_zero(unsigned& r) { r = 0u; }
-__device__ __forceinline__ void raw_zero(float& r) { r = 0.f; }
-__device__ __forceinline__ void raw_zero(float2& r) { r = make_float2(0.f, 0.f); }
+__device__ __forceinline__ void raw_zero(unsigned short& r, bool minus) { r = minus ? 0x8000 : 0; }
+__device__ __forceinline__ void raw_zero(unsigned& r, bool minus) { r = minus ? 0x80008000u : 0u; }
+__device__ __forceinline__ void raw_zero(float& r, bool minus) { r = minus ? -0.f : 0.f; }
+__device__ __forceinline__ void raw_zero(float2& r, bool minus) {
+  r.x = r.y = minus ? -0.f : 0.f;
+}
 __device__ __forceinline__ void widen(unsigned short r, float (&f)[1]) {
   f[0] = __uint_as_float((unsigned)r << 16);
 }
@@ -149,6 +151,10 @@ __device__ __forceinline__ float gate_b(float w, unsigned far, int i, float x) {
   if (MODE == GDN_GLR_INPUT_PLAIN) return x;
   return __fmul_rn(far >> i & 1 ? __fsub_rn(1.f, w) : -w, x);
 }
+
+// The zero x of an identity step, whose b is -0 (that of g is +0).
+template <int MODE>
+constexpr bool kGlrMinusX = MODE == GDN_GLR_INPUT_PLAIN;
 
 struct GlrArgs {
   const void* x;
@@ -402,9 +408,9 @@ struct GlrSource<T, V, true> {
     tile = stage + at.c * kGlrChunk * kGlrSlab + at.col;
   }
   __device__ __forceinline__ R get(int t) const { return raw_load<T, V>(tile + t * kGlrSlab); }
-  __device__ __forceinline__ void clear_from(int have) {
+  __device__ __forceinline__ void clear_from(int have, bool minus = false) {
     R zero;
-    raw_zero(zero);
+    raw_zero(zero, minus);
     for (int t = have; t < kGlrChunk; t++) *reinterpret_cast<R*>(tile + t * kGlrSlab) = zero;
   }
 };
@@ -414,14 +420,14 @@ struct GlrSource<T, V, false> {
   using R = typename Raw<T, V>::type;
   R r[kGlrChunk], next[kGlrChunk];
   // The loads of the chunk that the step after this one folds.
-  __device__ __forceinline__ void load(const T* row, int ld, int have) {
+  __device__ __forceinline__ void load(const T* row, int ld, int have, bool minus = false) {
     if (have == kGlrChunk) {
 #pragma unroll
       for (int t = 0; t < kGlrChunk; t++) next[t] = raw_load<T, V>(row_at(row, ld, t));
     } else {
 #pragma unroll
       for (int t = 0; t < kGlrChunk; t++) {
-        raw_zero(next[t]);
+        raw_zero(next[t], minus);
         if (t < have) next[t] = raw_load<T, V>(row_at(row, ld, t));
       }
     }
@@ -565,7 +571,7 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(true))
   auto load = [&](int t) {  // direct: the chunk at token t, ahead of its fold
     if constexpr (!STAGED) {
       const int have = at.live ? chunk_tokens(at, t) : 0;
-      sx.load(x + (int64_t)t * p.ldx, p.ldx, have);
+      sx.load(x + (int64_t)t * p.ldx, p.ldx, have, kGlrMinusX<MODE>);
       sg.load(g + (int64_t)t * p.ldg, p.ldg, have);
     }
   };
@@ -578,7 +584,7 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(true))
         sg.set(stage[pipe.slot].g, at);
         pipe.wait();
         if (tokens < kGlrChunk) {
-          sx.clear_from(tokens);
+          sx.clear_from(tokens, kGlrMinusX<MODE>);
           sg.clear_from(tokens);
         }
       } else {
@@ -881,7 +887,7 @@ __global__ void __launch_bounds__(kGlrShortThreads) k_glr_short_forward(const Gl
   GlrSource<G, 1, false> sg;
   auto load = [&](int t) {
     const int have = live && t < L ? min(kGlrChunk, L - t) : 0;
-    sx.load(x + (int64_t)t * p.ldx, p.ldx, have);
+    sx.load(x + (int64_t)t * p.ldx, p.ldx, have, kGlrMinusX<MODE>);
     sg.load(g + (int64_t)t * p.ldg, p.ldg, have);
   };
   load(0);

@@ -503,3 +503,30 @@ def test_two_threads_with_different_shapes(gdn):
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+@pytest.mark.parametrize("lens,D", [([2], 64), ([2], 37), ([130, 2], 64), ([2] * 64, 256)])
+def test_identity_steps_keep_the_sign_of_a_zero(gdn, lens, D):
+    """A sum that underflowed to -0 at a sequence's last token is -0 in its final
+    and decode state too.  x = (-2^-149, 0), a = exp(-1.4) < 1/2: B = -2^-149, then
+    fma(a, -2^-149, 0) rounds to -0, and h = fma(A, -0, -0) = -0."""
+    T, N = sum(lens), len(lens)
+    x = torch.zeros((T, D), device="cuda")
+    cu = W.cu_seqlens_of(lens, "cuda")
+    x[(cu[1:] - 2).long()] = -2.0 ** -149
+    g = torch.full((T, D), -1.4, device="cuda")
+    h0 = torch.full((N, D), -0.0, device="cuda")
+    state, steps = gdn.GlrDecodeState(N, D), gdn.GlrDecodeState(N, D)
+    h, fin, _, err = gdn.glr_forward(x, g, cu, h0=h0, state=state)
+    ok(gdn, err)
+    bits = lambda t: t.view(torch.int32)  # noqa: E731
+    last = (cu[1:] - 1).long()
+    assert torch.equal(bits(fin), bits(h[last]))
+    if max(lens) == 2:
+        assert (bits(fin) == -2 ** 31).all()
+        steps.h.copy_(h0)
+        for t in range(2):
+            hd = gdn.glr_decode_step(steps, x[last - 1 + t], g[last - 1 + t])
+            assert torch.equal(bits(hd), bits(h[last - 1 + t]))
+        for a, b in zip(steps.tensors(), state.tensors()):
+            assert torch.equal(bits(a), bits(b))
