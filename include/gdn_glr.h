@@ -27,9 +27,10 @@
  * no float atomics) with these differences: x, g, h and their gradients
  * [tokens, D] may have a row stride (ld*, in elements, >= D); they and the
  * contiguous fp32 arrays [rows, D] need only the alignment of their elements
- * (16 bytes for a decode state).  Rows that start on 16 bytes are the fast ones.  g may be -inf (a = 0); it must not be NaN or +inf.
+ * (16 bytes for a decode state).  Rows that start on 16 bytes are the fast ones.
+ * g may be -inf; it must not be NaN or +inf.  An a below 2^-126 counts as 0.
  * D is any size from 1 to 2^24, total_tokens up to 2^31 - 4097, strides up to
- * 2^27 elements.
+ * 2^27 elements, n_seqs ceil(D / 32) up to 2^28 - 1.
  */
 #ifndef GDN_GLR_H
 #define GDN_GLR_H

@@ -439,8 +439,8 @@ struct GlrSource<T, V, false> {
   __device__ __forceinline__ R get(int t) const { return r[t]; }
 };
 
-__device__ __forceinline__ void glr_prefetch(const GlrBoxes& box) {
-  for (const CUtensorMap* m : {&box.g, &box.x, &box.dh})
+__device__ __forceinline__ void glr_prefetch(const GlrBoxes& box, bool backward) {
+  for (const CUtensorMap* m : {&box.g, &box.x, backward ? &box.dh : &box.x})
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(true))
   unsigned char* smem = align128(smem_raw);
   Stage* stage = reinterpret_cast<Stage*>(smem);
   GlrPlace at;
-  if (STAGED && threadIdx.x == 0) glr_prefetch(box);
+  if (STAGED && threadIdx.x == 0) glr_prefetch(box, false);
   if (!glr_place<V>(p, at)) return;
   const int step_tokens = at.cs * kGlrTile;
   GlrMaps maps;
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(false))
   unsigned char* smem = align128(smem_raw);
   Stage* stage = reinterpret_cast<Stage*>(smem);
   GlrPlace at;
-  if (STAGED && threadIdx.x == 0) glr_prefetch(box);
+  if (STAGED && threadIdx.x == 0) glr_prefetch(box, true);
   if (!glr_place<V>(p, at)) return;
   const int step_tokens = at.cs * kGlrTile;
   GlrMaps maps;

@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kQkThreads, qk_backward_blocks(ROT, D))
         times8(e, w);
       }
       const float m = __fmul_rn(dot8<D>(n, e), p.inv_m);
-      const float z = -__fmul_rn(__fmul_rn(r, r), m);
+      const float z = -__fmul_rn(r, __fmul_rn(r, m));  // (r^2 may be out of range)
 #pragma unroll
       for (int j = 0; j < 4; j++) e.v[j] = __ffma2_rn(n.v[j], f2(z, z), e.v[j]);
       scale8(e, r);
@@ -634,7 +634,9 @@ extern "C" int gdn_qk_norm_backward(const void* q, int64_t ldq, const void* k, i
     if (!aligned(workspace, 16)) return GDN_ERR_INVALID_ARG;
   }
   gdn::QkArgs p{};
-  if (!gdn::qk_plan(p, T, Hq, Hk, d, weights ? gdn::qk_sums(rot_kind(rot_dim, interleaved), d) : 0)) return GDN_ERR_UNSUPPORTED;
+  const int rot = rot_kind(rot_dim, interleaved);
+  if (!gdn::qk_plan(p, T, Hq, Hk, d, weights ? gdn::qk_sums(rot, d) : 0))
+    return GDN_ERR_UNSUPPORTED;
   p.q.x = q, p.q.ldx = ldq, p.q.w = wq, p.q.dy = d_oq, p.q.lddy = lddoq, p.q.out = d_q;
   p.q.ldout = lddq;
   p.k.x = k, p.k.ldx = ldk, p.k.w = wk, p.k.dy = d_ok, p.k.lddy = lddok, p.k.out = d_k;
@@ -645,8 +647,8 @@ extern "C" int gdn_qk_norm_backward(const void* q, int64_t ldq, const void* k, i
   p.eps = eps;
   p.inv_m = norm == GDN_QK_NORM_RMS ? 1.f / (float)d : 1.f;
   p.partial = weights ? static_cast<float*>(workspace) : nullptr;
-  if (gdn::qk_types(true, p, in_dtype == GDN_BF16, grad_dtype == GDN_BF16, d,
-                    rot_kind(rot_dim, interleaved), st) != cudaSuccess)
+  if (gdn::qk_types(true, p, in_dtype == GDN_BF16, grad_dtype == GDN_BF16, d, rot, st) !=
+      cudaSuccess)
     return GDN_ERR_CUDA;
   if (weights) {
     if (gdn::launch_dependent(gdn::k_qk_weight_sum, dim3((unsigned)(d / 32), 2), dim3(1024), 0,

@@ -224,3 +224,14 @@ def test_idle_groups_add_nothing_to_the_weights(gdn, interleaved):
             opts = dict(norm="rms", interleaved=interleaved)
             close(grads["dw" + s], qk_norm.backward(x, dy, *rest, **opts)[1],
                   qk_norm.backward_bound(x, dy, *rest, **opts)[1])
+
+
+@pytest.mark.parametrize("norm", ["l2", "rms"])
+def test_smallest_eps(gdn, norm):
+    """A head of zeros with an eps whose r^2 is out of fp32's range: dx = r e."""
+    eps = float(np.float32(1e-42))
+    q, k, doq, dok, kw = draw(5, 3, 2, 64, 30)
+    q[1], k[:, 0] = 0, 0
+    grads = gdn.qk_norm_backward(q, k, doq, dok, norm=norm, eps=eps, **kw)
+    assert all(torch.isfinite(g).all() for g in grads.values())
+    check(gdn, q, k, doq, dok, kw, {"norm": norm, "eps": eps})
