@@ -503,13 +503,9 @@ class _Call:
         if not ok:
             raise ValueError(f"{self.what}: {why}")
 
-    def empty(self, shape, dtype, like=None):
-        """New memory for an output or scratch, used on the call's stream (`like`:
-        a tensor of that shape, and perhaps of that dtype)."""
-        if like is not None and like.dtype == dtype:
-            t = torch.empty_like(like, memory_format=torch.contiguous_format)
-        else:
-            t = torch.empty(shape, dtype=dtype, device=self.dev)
+    def empty(self, shape, dtype):
+        """New memory for an output or scratch, used on the call's stream."""
+        t = torch.empty(*shape, dtype=dtype, device=self.dev)  # (a tuple takes twice as long)
         if self.user_stream is not None:
             # the memory may have been freed on the current stream, whose work on it
             # is waited for; and it is kept from reuse until the call's stream is done
@@ -554,11 +550,11 @@ class _Call:
         t = self.empty(shape, dtype)
         return t, t.data_ptr()
 
-    def out_rows(self, t, name: str, shape, dtype, like):
+    def out_rows(self, t, name: str, shape, dtype):
         """The same for strided rows, which are always wanted."""
         if t is not None:
             return t, *self.rows(t, name, shape, dtype)
-        t = self.empty(shape, dtype, like)
+        t = self.empty(shape, dtype)
         return t, t.data_ptr(), (shape[1] if len(shape) == 2 else shape[1] * shape[2])
 
     def run(self, fn, *args):
@@ -624,7 +620,7 @@ def qk_norm_forward(q, k, *, norm: str = "l2", eps: float = 1e-6, wq=None, wk=No
         if x is None:
             out += [None, None, 0]
             continue
-        out += c.out_rows(o, name, (T, H, d), odt, x)
+        out += c.out_rows(o, name, (T, H, d), odt)
     c.run(lib.gdn_qk_norm_forward, *head, float(eps), *tail, int(bool(interleaved)), out[1],
           out[2], out[4], out[5], _dtype_code_of(odt))
     return out[0], out[3]
@@ -655,7 +651,7 @@ def qk_norm_backward(q, k, d_oq, d_ok, *, norm: str = "l2", eps: float = 1e-6, w
             continue
         gin += [*c.rows(g, "d_o" + s, (T, H, d), gdt)]
         given = grads["d" + s] if grads is not None else None
-        res["d" + s], *at = c.out_rows(given, "d" + s, (T, H, d), dt, x)
+        res["d" + s], *at = c.out_rows(given, "d" + s, (T, H, d), dt)
         gout += at
     for s, w in (("q", wq), ("k", wk)):
         given = grads["dw" + s] if grads is not None and w is not None and want_dw else None
@@ -758,7 +754,7 @@ def glr_forward(x, g, cu_seqlens, *, n_seqs: Optional[int] = None, h0=None,
     odt = _dtype_of(out_dtype, h.dtype if h is not None else x.dtype)
     f32 = torch.float32
     rows = glr_carry_rows(N, T)
-    h, hp, ldh = c.out_rows(h, "h", (T, D), odt, x)
+    h, hp, ldh = c.out_rows(h, "h", (T, D), odt)
     s_final, fin = c.out_full(s_final, want_state, "s_final", (N, D), f32)
     carry, car = c.out_full(carry, want_carry, "carry", (rows, D), f32)
     error, err = c.out_full(error, True, "error", (1,), torch.int32)
@@ -785,8 +781,8 @@ def glr_backward(x, g, cu_seqlens, carry, d_h, *, n_seqs: Optional[int] = None, 
     c.need(carry is not None, "carry is the forward's (want_carry=True)")
     car = c.full(carry, "carry", (glr_carry_rows(N, T), D), torch.float32)
     given = grads if grads is not None else {}
-    dx, dxp, lddx = c.out_rows(given.get("dx"), "dx", (T, D), x.dtype, x)
-    dg, dgp, lddg = c.out_rows(given.get("dg"), "dg", (T, D), g.dtype, g)
+    dx, dxp, lddx = c.out_rows(given.get("dx"), "dx", (T, D), x.dtype)
+    dg, dgp, lddg = c.out_rows(given.get("dg"), "dg", (T, D), g.dtype)
     dh0, dhp0 = c.out_full(given.get("dh0"), want_dh0 and grads is None, "dh0", (N, D),
                            torch.float32)
     if grads is None:
@@ -807,7 +803,7 @@ def glr_decode_step(state: GlrDecodeState, x, g, *, slot_idx=None, complement: b
     B, D = x.shape
     ins = _glr_inputs(c, x, g)
     odt = _dtype_of(out_dtype, h.dtype if h is not None else x.dtype)
-    h, hp, ldh = c.out_rows(h, "h", (B, D), odt, x)
+    h, hp, ldh = c.out_rows(h, "h", (B, D), odt)
     c.run(lib.gdn_glr_decode_step, *ins, c.full(slot_idx, "slot_idx", (B,), torch.int32), B, D,
           _glr_mode(complement), _glr_state(c, state, D), hp, ldh, _dtype_code_of(odt))
     return h
