@@ -583,7 +583,7 @@ def _norm_kind(norm: str) -> int:
 
 def _qk_call(what, q, k, norm, wq, wk, positions, inv_freq, stream):
     some = q if q is not None else k
-    if some is None or any(t is not None and t.dim() != 3 for t in (q, k)):
+    if (some is None or some.dim() != 3) or (k is not None and k.dim() != 3):
         raise ValueError(f"{what}: q, k must be [tokens, heads, d] (one of them may be None)")
     c = _Call(what, some, stream)
     T, _, d = some.shape
@@ -673,12 +673,14 @@ def qk_norm_backward(q, k, d_oq, d_ok, *, norm: str = "l2", eps: float = 1e-6, w
     return res
 
 
+_CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+
+
 def _dtype_code_of(dtype) -> int:
-    if dtype == torch.bfloat16:
-        return GDN_BF16
-    if dtype == torch.float32:
-        return GDN_F32
-    raise ValueError(f"gdn_cpr: unsupported dtype {dtype}")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"gdn_cpr: unsupported dtype {dtype}")
+    return code
 
 
 class GlrDecodeState:
