@@ -221,20 +221,30 @@ __device__ __forceinline__ QkUnit qk_unit(const QkSide& sd, int64_t u, int64_t e
 
 // Heads whose loads are under way together, and the blocks of a multiprocessor
 // that their registers are kept to.  10240 x (16 + 16) heads of 128, no
-// rotation: forward 29 us with 4 heads and 5 blocks (2 heads: 31), backward 57 us
+// rotation: forward 29 us with 4 heads and 5 blocks (2 heads: 31), backward 53 us
 // with 2 heads and 3 blocks (4 heads and 2 blocks: 64, 1 and 4: 68).  16384 x
-// (32 + 8) rotated with weights: forward 61 us (78 without the bound), backward
-// 104 us with 4 heads and 2 blocks (2 and 3: 109, 1 and 4: 131); 8192 x (8 + 2)
-// heads of 256: 37 us with 2 and 3 (4 and 2: 53).
+// (32 + 8) rotated with weights: forward 60 us (78 without the bound).  8192 x
+// (8 + 2) heads of 256: backward 37 us with 2 and 3 (4 and 2: 53).
+//
+// A rotation's backward has registers for 2 blocks only, whose warps do not
+// cover each other's loads: it has the next batch under way while it works on
+// one (16384 x (32 + 8): 100 us, without it 104; fp32, 8192 x (16 + 4): 47, 49).
+// Two batches of 4 heads fit where all elements are bf16 (2 heads: 103), else 2
+// (8192 x (16 + 16) heads of 64 with fp32 gradients: 30 us, 4 heads 42).  Without
+// a rotation, and with heads of 256, 3 blocks do better (53 against 61 us, 37
+// against 42).
 constexpr int kQkForwardBatch = 4;
 __host__ __device__ constexpr int qk_forward_blocks(int rot, size_t element) {
   return rot == kRotNone ? 5 : element == 2 ? 4 : 3;
 }
-__host__ __device__ constexpr int qk_backward_batch(int rot, int d) {
-  return rot == kRotNone || d == 256 ? 2 : 4;
+__host__ __device__ constexpr bool qk_backward_ahead(int rot, int d) {
+  return rot != kRotNone && d != 256;
+}
+__host__ __device__ constexpr int qk_backward_batch(int rot, int d, size_t elements) {
+  return qk_backward_ahead(rot, d) && elements == 4 ? 4 : 2;
 }
 __host__ __device__ constexpr int qk_backward_blocks(int rot, int d) {
-  return rot == kRotNone || d == 256 ? 3 : 2;
+  return qk_backward_ahead(rot, d) ? 2 : 3;
 }
 
 template <class IN, class OUT, int D, int ROT>
@@ -313,7 +323,9 @@ __global__ void __launch_bounds__(kQkThreads, qk_forward_blocks(ROT, sizeof(IN))
 template <class IN, class GR, int D, int ROT>
 __global__ void __launch_bounds__(kQkThreads, qk_backward_blocks(ROT, D))
     k_qk_backward(const QkArgs p) {
-  constexpr int kLanes = D / 8, kGroups = kQkThreads / kLanes, kBatch = qk_backward_batch(ROT, D);
+  constexpr int kLanes = D / 8, kGroups = kQkThreads / kLanes;
+  constexpr int kBatch = qk_backward_batch(ROT, D, sizeof(IN) + sizeof(GR));
+  constexpr bool kAhead = qk_backward_ahead(ROT, D);
   extern __shared__ uint64_t freq[];  // [F], and each group's [F] cosines and sines
   const bool isq = blockIdx.x < p.q.blocks;
   const QkSide& sd = isq ? p.q : p.k;
@@ -332,37 +344,42 @@ __global__ void __launch_bounds__(kQkThreads, qk_backward_blocks(ROT, D))
   if (sd.w) weights8(sd.w, l, w);
   using RawX = typename Four<IN>::type;
   using RawG = typename Four<GR>::type;
-  for (int64_t base = first; base < end; base += kGroups) {
-    const QkUnit u = qk_unit(sd, base + grp, end);
-    const IN* x = static_cast<const IN*>(sd.x) + u.t * sd.ldx + (int64_t)u.h0 * D;
-    const GR* dy = static_cast<const GR*>(sd.dy) + u.t * sd.lddy + (int64_t)u.h0 * D;
-    IN* dx = static_cast<IN*>(sd.out) + u.t * sd.ldout + (int64_t)u.h0 * D;
-    const IN *px = x + l.a, *qx = x + l.b;
-    const GR *pg = dy + l.a, *qg = dy + l.b;
-    IN *pd = dx + l.a, *qd = dx + l.b;
-    Turn turn;
+  struct Batch {  // of a unit's heads, as loaded
     RawX xa[kBatch], xb[kBatch];
     RawG ga[kBatch], gb[kBatch];
-    auto load = [&](int left, bool full) {
+  };
+  Batch cur;
+  Turn turn;
+  QkUnit u = qk_unit(sd, first + grp, end);
+  const IN* x = static_cast<const IN*>(sd.x) + u.t * sd.ldx + (int64_t)u.h0 * D;
+  const GR* dy = static_cast<const GR*>(sd.dy) + u.t * sd.lddy + (int64_t)u.h0 * D;
+  auto load = [&](Batch& b, const IN* x, const GR* dy, int left, bool full) {
+    const IN *px = x + l.a, *qx = x + l.b;
+    const GR *pg = dy + l.a, *qg = dy + l.b;
 #pragma unroll
-      for (int i = 0; i < kBatch; i++) {
-        if (full || i < left) {
-          xa[i] = *reinterpret_cast<const RawX*>(px + i * D);
-          xb[i] = *reinterpret_cast<const RawX*>(qx + i * D);
-          ga[i] = *reinterpret_cast<const RawG*>(pg + i * D);
-          gb[i] = *reinterpret_cast<const RawG*>(qg + i * D);
-        } else {  // zeros: nothing for dw
-          xa[i] = xb[i] = RawX{};
-          ga[i] = gb[i] = RawG{};
-        }
+    for (int i = 0; i < kBatch; i++) {
+      if (full || i < left) {
+        b.xa[i] = *reinterpret_cast<const RawX*>(px + i * D);
+        b.xb[i] = *reinterpret_cast<const RawX*>(qx + i * D);
+        b.ga[i] = *reinterpret_cast<const RawG*>(pg + i * D);
+        b.gb[i] = *reinterpret_cast<const RawG*>(qg + i * D);
+      } else {  // zeros: nothing for dw
+        b.xa[i] = b.xb[i] = RawX{};
+        b.ga[i] = b.gb[i] = RawG{};
       }
-    };
+    }
+  };
+  bool full = __all_sync(kFull, u.heads >= kBatch);
+  load(cur, x, dy, u.heads, full);
+  for (int64_t base = first; base < end; base += kGroups) {
+    IN* dx = static_cast<IN*>(sd.out) + u.t * sd.ldout + (int64_t)u.h0 * D;
+    IN *pd = dx + l.a, *qd = dx + l.b;
     auto head = [&](int i, bool write) {
       Eight n, e;  // the head and its gradient
-      widen4(xa[i], n.v);
-      widen4(xb[i], n.v + 2);
-      widen4(ga[i], e.v);
-      widen4(gb[i], e.v + 2);
+      widen4(cur.xa[i], n.v);
+      widen4(cur.xb[i], n.v + 2);
+      widen4(cur.ga[i], e.v);
+      widen4(cur.gb[i], e.v + 2);
       rotate8<ROT>(e, l, turn);
       const float r = rsqrtf(__fmaf_rn(dot8<D>(n, n), p.inv_m, p.eps));
       if (sd.w) {
@@ -382,23 +399,36 @@ __global__ void __launch_bounds__(kQkThreads, qk_backward_blocks(ROT, D))
         store4(qd + i * D, e.v + 2);
       }
     };
-    bool full = __all_sync(kFull, u.heads >= kBatch);
-    load(u.heads, full);
     qk_angles<D, ROT, -1>(p, l, u.have, u.t, freq, table, turn);
+    const int heads = u.heads;
     for (int h = 0; h < sd.heads; h += kBatch) {
-      if (full) {
+      const bool now = full;
+      auto load_next = [&](Batch& b) {  // the unit's next batch, or the next unit's first
+        int left = heads - h - kBatch;
+        x += kBatch * D, dy += kBatch * D;
+        if (h + kBatch >= sd.heads) {
+          u = qk_unit(sd, base + kGroups + grp, end);
+          left = u.heads;
+          x = static_cast<const IN*>(sd.x) + u.t * sd.ldx + (int64_t)u.h0 * D;
+          dy = static_cast<const GR*>(sd.dy) + u.t * sd.lddy + (int64_t)u.h0 * D;
+        }
+        full = __all_sync(kFull, left >= kBatch);
+        load(b, x, dy, left, full);
+      };
+      Batch next;
+      if (kAhead) load_next(next);
+      if (now) {
 #pragma unroll
         for (int i = 0; i < kBatch; i++) head(i, true);
       } else {
 #pragma unroll
-        for (int i = 0; i < kBatch; i++) head(i, h + i < u.heads);
+        for (int i = 0; i < kBatch; i++) head(i, h + i < heads);
       }
-      px += kBatch * D, qx += kBatch * D, pg += kBatch * D, qg += kBatch * D;
       pd += kBatch * D, qd += kBatch * D;
-      if (h + kBatch < sd.heads) {
-        full = __all_sync(kFull, u.heads >= h + 2 * kBatch);
-        load(u.heads - h - kBatch, full);
-      }
+      if (kAhead)
+        cur = next;
+      else
+        load_next(cur);
     }
   }
   if (p.partial && sd.w) {  // the block's sum of dw over its groups, in ascending order
