@@ -163,6 +163,7 @@ struct GlrArgs {
   const int32_t* cu;
   int N;
   int T, D, slabs, stages;
+  bool longest_first;  // tile kernels: the grid's order of the sequences
   const float* h0;  // forward
   void* h;
   int ldh;
@@ -193,6 +194,28 @@ __device__ __forceinline__ bool glr_seq(const GlrArgs& p, int n, int& start, int
   start = first;
   length = end - first;
   return (zero == 0) & (total == p.T) & (first >= 0) & (end >= first) & (end <= p.T);
+}
+
+// The sequence with the r-th most tokens (the earlier of two as long as each
+// other), for up to 32 of them: lane i of every warp finds the rank of sequence
+// i.  Where blocks wait for a place, the longest then start first.  Any
+// cu_seqlens give a permutation.
+constexpr int kGlrOrder = 32;
+__device__ __forceinline__ bool glr_seq_by_length(const GlrArgs& p, int r, int& n, int& start,
+                                                  int& length) {
+  const int i = threadIdx.x & 31, zero = p.cu[0], total = p.cu[p.N];
+  const int first = i < p.N ? p.cu[i] : 0, end = i < p.N ? p.cu[i + 1] : 0;
+  const int tokens = (int)((unsigned)end - (unsigned)first);
+  int rank = 0;
+  for (int j = 0; j < p.N; j++) {
+    const int other = __shfl_sync(kFull, tokens, j);
+    rank += other > tokens || (other == tokens && j < i);
+  }
+  n = __ffs(__ballot_sync(kFull, i < p.N && rank == r)) - 1;
+  start = __shfl_sync(kFull, first, n);
+  const int stop = __shfl_sync(kFull, end, n);
+  length = stop - start;
+  return (zero == 0) & (total == p.T) & (start >= 0) & (stop >= start) & (stop <= p.T);
 }
 
 // Slot of row n, or -1 when it is out of range or an earlier row has it too.
@@ -233,7 +256,7 @@ __device__ __forceinline__ void glr_report(const GlrArgs& p) {
 }
 
 // Where a thread stands: its block takes tile rank, rank + cs, ... of slab
-// `slab` of sequence n; the thread channels ch .. ch + V - 1 of chunk c.
+// `slab` of sequence n (at first: the n-th in the grid's order); the thread channels ch .. ch + V - 1 of chunk c.
 struct GlrPlace {
   int n, slab, rank, cs, c, col, ch;
   bool live;
@@ -248,7 +271,10 @@ __device__ __forceinline__ bool glr_place(const GlrArgs& p, GlrPlace& at) {
   at.n = unit / p.slabs;
   at.slab = unit % p.slabs;
   glr_report(p);
-  if (!glr_seq(p, at.n, at.start, at.L)) return false;  // the same for a whole cluster
+  // (both the same for a whole cluster)
+  if (p.longest_first ? !glr_seq_by_length(p, at.n, at.n, at.start, at.L)
+                      : !glr_seq(p, at.n, at.start, at.L))
+    return false;
   at.c = threadIdx.x / (kGlrSlab / V);
   at.col = threadIdx.x % (kGlrSlab / V) * V;
   at.ch = at.slab * kGlrSlab + at.col;
@@ -1088,6 +1114,8 @@ static unsigned glr_step_threads(int D) {
 // ----------------------------------------------------------------------------
 enum GlrOp { kGlrFwd, kGlrBwd, kGlrStep };
 
+constexpr size_t kGlrStatic = 4608;  // shared memory of a block that its launch does not size
+
 // Launch shape.  Blocks of a cluster: doubled while every block of the grid
 // still has a place on the device and a sequence has tiles for them on average
 // (65536 x 2048 alone, forward: 373, 252, 178 us with 1, 2 and 4; 8 have no
@@ -1100,10 +1128,15 @@ enum GlrOp { kGlrFwd, kGlrBwd, kGlrStep };
 // x 1000 in 9 sequences: 84 against 72 us); where blocks are many the others
 // cover that, and three blocks with two stages win (16384 x 2048 in 32: 90
 // against 107 us).
-constexpr size_t kGlrStatic = 4608;  // shared memory of a block that its launch does not size
-
+//
+// Longest sequences first where some blocks have to wait for a place: 10240
+// tokens of 2048 channels in sequences of 531, 793, 1762, 2136 and 5018, forward
+// and backward: 92 us (without it 115); where it gains nothing, 16384 x 2048 in
+// 32 equal ones: 145 (141).  With 64 sequences every block's search for its own
+// cost more than the order gained (57344 x 4096: 913 against 900 us).
 struct GlrShape {
   int cs, stages;
+  bool longest_first;
   size_t smem;
 };
 
@@ -1117,23 +1150,27 @@ static GlrShape glr_shape(const GlrArgs& p, size_t stage, int most, bool backwar
   };
   const int64_t units = (int64_t)p.N * p.slabs;
   const int max_cluster = backward ? 4 : 8;
-  GlrShape sh{1, 0, 0};
+  GlrShape sh{1, 0, false, 0};
   while (sh.cs < max_cluster && units * 2 * sh.cs <= places(2 * sh.cs) &&
          p.T > (int64_t)p.N * kGlrTile * sh.cs)
     sh.cs *= 2;
   // Sequences of unequal length keep the device waiting for the longest: two
   // blocks for each then gain more than a second wave of blocks costs (10240
-  // tokens of 2048 channels in 5 sequences, forward and backward: 100 against 145
-  // us where they are uneven, 100 against 86 us where they are equal).
-  if (sh.cs == 1 && p.N > 1 && units <= most * kSms && p.T > (int64_t)p.N * kGlrTile) sh.cs = 2;
+  // tokens of 2048 channels in 5 sequences, forward and backward: 92 against 145
+  // us where they are uneven, 100 against 88 us where they are equal), for a
+  // backward from a few more units on (20000 x 2048 in 9, uneven: 104 against 133
+  // us, 18432 in 9 equal ones: 94 against 104; the forward the same within 2 us).
+  const int waves = backward && stage > 0 ? 4 : most;
+  if (sh.cs == 1 && p.N > 1 && units <= waves * kSms && p.T > (int64_t)p.N * kGlrTile) sh.cs = 2;
+  int64_t here = (units * sh.cs + kSms - 1) / kSms;  // blocks of a multiprocessor
+  here = here < most ? here : most;
   if (stage > 0) {
     const size_t fixed = kBlock + maps(sh.cs), least = backward && sh.cs > 1 ? 3 : 2;
-    int64_t here = (units * sh.cs + kSms - 1) / kSms;
-    here = here < most ? here : most;
     while (here > 1 && kSmem / here < fixed + least * stage) here--;
     sh.stages = (int)((kSmem / here - fixed) / stage);
     if (sh.stages > kGlrMaxStages) sh.stages = kGlrMaxStages;
   }
+  sh.longest_first = p.N > 1 && p.N <= kGlrOrder && units * sh.cs > here * kSms;
   sh.smem = sh.stages * stage + maps(sh.cs);
   return sh;
 }
@@ -1143,6 +1180,7 @@ static cudaError_t glr_run(K kernel, int threads, size_t stage, int most, bool b
                            GlrArgs& p, const GlrBoxes& box, cudaStream_t st) {
   const GlrShape sh = glr_shape(p, stage, most, backward);
   p.stages = sh.stages;
+  p.longest_first = sh.longest_first;
   // The kernel's limit, not this call's size: two host threads may be here at once.
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        227 * 1024 - (int)kGlrStatic);

@@ -530,3 +530,41 @@ def test_identity_steps_keep_the_sign_of_a_zero(gdn, lens, D):
             assert torch.equal(bits(hd), bits(h[last - 1 + t]))
         for a, b in zip(steps.tensors(), state.tensors()):
             assert torch.equal(bits(a), bits(b))
+
+
+@pytest.mark.parametrize("lens", [[300, 5, 300, 0, 129, 700, 17, 300] * 4, [40, 900, 0, 900, 900]])
+def test_batches_whose_longest_start_first(gdn, lens):
+    """More blocks than places: sequences of equal and no length, their decode
+    states, and a batch with a bad sequence, whose others are not touched by it."""
+    D, N = 2048, len(lens)
+    x, g, dh, h0, ds, cu = draw(lens, D, 71)
+    slots = torch.arange(N, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    state = gdn.GlrDecodeState(N, D)
+    h, fin, carry, err = gdn.glr_forward(x, g, cu, h0=h0, state=state, slot_idx=slots,
+                                         want_carry=True)
+    ok(gdn, err)
+    grads, err = gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds)
+    ok(gdn, err)
+    edges = cu.tolist()
+    for n in sorted({*range(6), N - 2, N - 1} & set(range(N))):
+        rows = slice(edges[n], edges[n + 1])
+        one = gdn.GlrDecodeState(1, D)
+        c = W.cu_seqlens_of([lens[n]], "cuda")
+        h1, f1, c1, _ = gdn.glr_forward(x[rows], g[rows], c, h0=h0[n:n + 1], state=one,
+                                        want_carry=True)
+        g1, _ = gdn.glr_backward(x[rows], g[rows], c, c1, dh[rows], ds_final=ds[n:n + 1])
+        assert torch.equal(h1, h[rows]) and torch.equal(f1[0], fin[n])
+        assert torch.equal(g1["dx"], grads["dx"][rows])
+        assert torch.equal(g1["dg"], grads["dg"][rows])
+        assert torch.equal(g1["dh0"][0], grads["dh0"][n])
+        for a, b in zip(one.tensors(), state.tensors()):
+            assert torch.equal(a[0], b[slots[n]])
+    # sequence 1 ends before it starts: it and the next, which then overlaps 0, are not looked at
+    bad = cu.clone()
+    bad[2] = 0
+    out = torch.full_like(h, 7.0)
+    _, f2, _, err = gdn.glr_forward(x, g, bad, h0=h0, h=out)
+    assert err.item() == gdn.GDN_DEVERR_CU_SEQLENS
+    for n in range(3, N):
+        rows = slice(edges[n], edges[n + 1])
+        assert torch.equal(out[rows], h[rows]) and torch.equal(f2[n], fin[n])
