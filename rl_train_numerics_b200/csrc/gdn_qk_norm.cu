@@ -11,6 +11,12 @@
 // A group takes some heads of one token at a time: the token's cosines and
 // sines, computed once by the group's lanes and exchanged, stay in registers
 // with the weights, and the loads of several heads are under way together.
+//
+// Memory bounds it: each head is read once and written once (backward: two reads
+// and a write).  32768 x (16 + 16) bf16 heads of 128: 85 us forward, 169 with an
+// fp32 gradient backward, 6.3 TB/s each of 6.5 that a copy reaches.  A rotation with
+// weights adds instructions (62 a head forward, 79 backward): 16384 x (32 + 8)
+// takes 60 us (5.6 TB/s) and 100 us (5.0 TB/s).
 #include <cuda_runtime.h>
 #include <math.h>
 
