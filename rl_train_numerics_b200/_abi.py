@@ -696,10 +696,6 @@ class GlrDecodeState:
         self.pos = torch.zeros((n_slots,), dtype=torch.int32, device=device)
         self.error = torch.zeros((1,), dtype=torch.int32, device=device)
 
-    def struct(self) -> GlrStateStruct:
-        return GlrStateStruct(self.h.data_ptr(), self.a.data_ptr(), self.b.data_ptr(),
-                              self.pos.data_ptr(), self.error.data_ptr(), self.n_slots)
-
     def tensors(self):
         return (self.h, self.a, self.b, self.pos)
 
@@ -711,11 +707,13 @@ class GlrDecodeState:
 
 
 def _glr_state(c: _Call, state: GlrDecodeState, D: int) -> GlrStateStruct:
-    for name in ("h", "a", "b"):
-        c.full(getattr(state, name), "state." + name, (state.n_slots, D), torch.float32)
-    c.full(state.pos, "state.pos", (state.n_slots,), torch.int32)
-    c.full(state.error, "state.error", (1,), torch.int32)
-    return state.struct()
+    n = state.n_slots
+    shape = (n, D)
+    return GlrStateStruct(c.full(state.h, "state.h", shape, torch.float32),
+                          c.full(state.a, "state.a", shape, torch.float32),
+                          c.full(state.b, "state.b", shape, torch.float32),
+                          c.full(state.pos, "state.pos", (n,), torch.int32),
+                          c.full(state.error, "state.error", (1,), torch.int32), n)
 
 
 def _glr_inputs(c: _Call, x, g):
