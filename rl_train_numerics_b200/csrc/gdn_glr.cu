@@ -26,10 +26,10 @@
 // sequences: 48 us (5.6 TB/s) and 77 us (6.1 TB/s, of 6.5 that a copy reaches);
 // 57344 x 4096 in 64 uneven ones: 310 and 591 us (6.1 and 5.6 TB/s).  A sequence
 // alone is bound by its steps, one after the other: 65536 x 2048 with bf16 gates
-// takes 181 and 255 us (4.4 and 5.3 TB/s), 32768 x 1024 73 and 118.  Chunks of 16 tokens keep
-// the maps of two channels (64 floats) in a thread's registers from the fold to
-// the write, at three blocks of a multiprocessor; slabs of 32 channels make a
-// token's row of a box a whole 128-byte line of fp32.
+// takes 181 and 255 us (4.4 and 5.3 TB/s), 32768 x 1024 73 and 118.  Chunks of 16
+// tokens keep the maps of two channels (64 floats) in a thread's registers from
+// the fold to the write, at three blocks of a multiprocessor; slabs of 32
+// channels make a token's row of a box a whole 128-byte line of fp32.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -266,7 +266,7 @@ __device__ __forceinline__ void glr_report(const GlrArgs& p) {
 }
 
 // Where a thread stands: its block takes tile rank, rank + cs, ... of slab
-// `slab` of sequence n (at first: the n-th in the grid's order); the thread channels ch .. ch + V - 1 of chunk c.
+// `slab` of sequence n; the thread channels ch .. ch + V - 1 of chunk c.
 struct GlrPlace {
   int n, slab, rank, cs, c, col, ch;
   bool live;
@@ -278,13 +278,13 @@ __device__ __forceinline__ bool glr_place(const GlrArgs& p, GlrPlace& at) {
   at.cs = (int)cg::this_cluster().num_blocks();
   at.rank = (int)cg::this_cluster().block_rank();
   const int unit = blockIdx.x / at.cs;
-  at.n = unit / p.slabs;
+  const int turn = unit / p.slabs;
   at.slab = unit % p.slabs;
   glr_report(p);
-  // (both the same for a whole cluster)
-  if (p.longest_first ? !glr_seq_by_length(p, at.n, at.n, at.start, at.L)
-                      : !glr_seq(p, at.n, at.start, at.L))
-    return false;
+  at.n = turn;
+  const bool valid = p.longest_first ? glr_seq_by_length(p, turn, at.n, at.start, at.L)
+                                     : glr_seq(p, at.n, at.start, at.L);
+  if (!valid) return false;  // the same for a whole cluster
   at.c = threadIdx.x / (kGlrSlab / V);
   at.col = threadIdx.x % (kGlrSlab / V) * V;
   at.ch = at.slab * kGlrSlab + at.col;
