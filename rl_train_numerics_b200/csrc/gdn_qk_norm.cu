@@ -230,7 +230,10 @@ __device__ __forceinline__ QkUnit qk_unit(const QkSide& sd, int64_t u, int64_t e
 // rotation: forward 29 us with 4 heads and 5 blocks (2 heads: 31), backward 53 us
 // with 2 heads and 3 blocks (4 heads and 2 blocks: 64, 1 and 4: 68).  16384 x
 // (32 + 8) rotated with weights: forward 60 us (78 without the bound).  8192 x
-// (8 + 2) heads of 256: backward 37 us with 2 and 3 (4 and 2: 53).
+// (8 + 2) heads of 256: backward 37 us with 2 and 3 (4 and 2: 53).  fp32 heads are
+// twice the registers: forward of 16384 x (32 + 8) without rotation 100 us with 3
+// blocks (1.0 of the copy rate; 5: 144, they spill), 8192 x (16 + 16) to bf16 33
+// (52), 16384 x (16 + 8) of 64 31 (50).
 //
 // A rotation's backward has registers for 2 blocks only, whose warps do not
 // cover each other's loads: it has the next batch under way while it works on
@@ -241,7 +244,7 @@ __device__ __forceinline__ QkUnit qk_unit(const QkSide& sd, int64_t u, int64_t e
 // against 42).
 constexpr int kQkForwardBatch = 4;
 __host__ __device__ constexpr int qk_forward_blocks(int rot, size_t element) {
-  return rot == kRotNone ? 5 : element == 2 ? 4 : 3;
+  return element == 4 ? 3 : rot == kRotNone ? 5 : 4;
 }
 __host__ __device__ constexpr bool qk_backward_ahead(int rot, int d) {
   return rot != kRotNone && d != 256;
