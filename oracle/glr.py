@@ -56,17 +56,31 @@ def backward(x, g, lengths, d_h, h0=None, ds_final=None, complement=False):
 
 
 # One step of an fp32 evaluation multiplies every older term by a decay that is
-# off by at most (4 + 1.25 |g|) U (2^x off by 4 U, the rounding of x = g log2 e by
-# |g| U and that of the constant by |g| U / 4; 1 + e of the complement form by less),
-# with one rounding of the running product and one of the running sum:
-# (6 + 1.25 |g|) U.  A term starts with the rounding of its input ((1 - a) x: at
-# most 14 U) and ends with those of the state's last operations: 16 U.  First
-# order; the factor 1.01 covers the products of roundings at these lengths.
+# off by
+#   |g| < 1/8, plain: the series 1 + g s, whose rest is 0.1 U of a and whose s is
+#     off by 1.1 U (half a step of s, which may be above 1, and |g| times the step
+#     before), that is 0.14 U of a, and half a step of a (U above 1): 1.4 U
+#   |g| < 1/2, complement: e = exp(g) - 1 is off by 2.9 U of itself (s by 1.7 U, its
+#     product with g by U, the rest 0.25 U), at most 1.9 U of a = 1 + e, whose
+#     rounding is at most 0.83 U below 1 and U above: 2.9 U
+#   else (4 + 1.25 |g|) U: 2^x off by 4 U, the rounding of x = g log2 e by |g| U and
+#     that of the constant by |g| U / 4
+# and adds one rounding of the running product and one of the running sum: 2 U.
+# A term starts with the rounding of its input ((1 - a) x: at most 14 U) and ends
+# with those of the state's last operations: 16 U.  First order; the factor 1.01
+# covers the products of roundings at these lengths.
 ENDS = 16.0 * 1.01 * U
 
 
-def _step(g):
-    return 1.01 * U * (6.0 + 1.25 * np.minimum(np.abs(np.asarray(g, np.float64)), 200.0))
+def decay_bound(g, complement=False):
+    """Bound of an fp32 decay's relative error."""
+    size = np.abs(np.asarray(g, np.float64))
+    near, most = (0.5, 2.9) if complement else (0.125, 1.4)
+    return U * np.where(size < near, most, 4.0 + 1.25 * np.minimum(size, 200.0))
+
+
+def _step(g, complement):
+    return 1.01 * (decay_bound(g, complement) + 2.0 * U)
 
 
 def _aged(a, step, b, s0, lengths, reverse=False):
@@ -93,7 +107,7 @@ def _aged(a, step, b, s0, lengths, reverse=False):
 
 def forward_bound(x, g, lengths, h0=None, complement=False):
     """Elementwise bounds of |h - fp32 h| and |s_final - fp32 s_final|."""
-    step = _step(g)
+    step = _step(g, complement)
     x, a, gain = _parts(x, g, complement)
     z = np.zeros((len(lengths), x.shape[1])) if h0 is None else np.asarray(h0, np.float64)
     S, W, fs, fw = _aged(a, step, gain * x, z, lengths)
@@ -104,7 +118,7 @@ def backward_bound(x, g, lengths, d_h, h0=None, ds_final=None, complement=False)
     """Elementwise bounds of an fp32 (dx, dg, dh0)."""
     eh, _ = forward_bound(x, g, lengths, h0, complement)
     h, _ = forward(x, g, lengths, h0, complement)
-    step = _step(g)
+    step = _step(g, complement)
     x, a, gain = _parts(x, g, complement)
     D = x.shape[1]
     z = np.zeros((len(lengths), D))

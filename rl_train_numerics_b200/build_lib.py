@@ -20,7 +20,9 @@ NVCC_FLAGS = [
     "-O3", "-lineinfo", "-std=c++17",
     # One flag set for every kernel: IEEE fp32 (no fast math, no flush to zero,
     # correctly rounded division and square root) and no implicit
-    # multiply-add contraction; the kernels spell out every fused op.
+    # multiply-add contraction; the kernels spell out every fused op.  (Two call
+    # an approximate function by name: gdn_glr.cu ex2.approx.ftz, for gates away
+    # from 0, and gdn_qk_norm.cu rsqrtf.)
     "--fmad=false", "-ftz=false", "-prec-div=true", "-prec-sqrt=true",
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",

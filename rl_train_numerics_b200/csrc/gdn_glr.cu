@@ -114,42 +114,65 @@ __device__ __forceinline__ typename Raw<T, V>::type raw_load(const T* p) {
   return *reinterpret_cast<const typename Raw<T, V>::type*>(p);
 }
 
-// a = exp(g) as 2^(g log2 e), by ex2.approx (relative error at most 2^-22 = 4 U,
-// U = 2^-24).  The rounded product adds |g| U and the rounded constant |g| U / 4
-// to it, relative to a: a weight of e^-G carries an error of at most 1.25 G U
-// e^-G < U / 2 of what it weighs, so the states are as good as with an exact
-// exponential, for 2 instructions.  -inf gives 0, a NaN stays one.
-__device__ __forceinline__ float decay(float g) {
+// a = exp(g).  Far from 0 as 2^(g log2 e) by ex2.approx: a relative error of at
+// most 2^-22 = 4 U (U = 2^-24), with |g| U for the rounded product and |g| U / 4
+// for the rounded constant.  A state is a sum of inputs weighted by products of
+// decays; where every |g| is at least 1/8, those errors change it by at most
+// (4 U + 1.25 |g| U) / (1 - a) < 36 U.  -inf gives 0, a NaN stays one.
+__device__ __forceinline__ float decay_far(float g) {
   float a;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(__fmul_rn(g, 1.4426950408889634f)));
   return a;
 }
+// a for |g| < 1/8: the Taylor series to g^5 / 5!.  A slow gate's error is not
+// washed out by its own decay: a state that lives 1 / |g| tokens takes it up
+// as often.  Here the rest of the series is 0.1 U of a, a product with |g| < 1/8
+// scales down the roundings before the last, and the last is half a step: 0.8 U
+// below 1 (1.4 U above), and half a step alone for g towards 0, without a bias
+// (ex2.approx: 2.3 U and a bias of -0.3 U measured over [-1/2, 0], expf 2.3 and
+// +0.2).  Two gates at a time, packed: forward and backward of 65536 x 2048
+// alone 446 us (433 without it), of 10240 x 2048 in 5 uneven sequences 96 (95).
+// expf, exact to 2 U everywhere, takes 490 and 98.
+__device__ __forceinline__ float2 decay_near(float2 g) {
+  float2 s = f2(1.f / 120.f, 1.f / 120.f);
+  s = __ffma2_rn(s, g, f2(1.f / 24.f, 1.f / 24.f));
+  s = __ffma2_rn(s, g, f2(1.f / 6.f, 1.f / 6.f));
+  s = __ffma2_rn(s, g, f2(0.5f, 0.5f));
+  s = __ffma2_rn(s, g, f2(1.f, 1.f));
+  return __ffma2_rn(s, g, f2(1.f, 1.f));
+}
 // exp(g) - 1 for |g| <= 1/2: the Taylor series to g^8 / 8! (the rest is below
 // 2^-26 of it).
-__device__ __forceinline__ float decay_m1(float g) {
-  float s = 1.f / 40320.f;
-  s = __fmaf_rn(s, g, 1.f / 5040.f);
-  s = __fmaf_rn(s, g, 1.f / 720.f);
-  s = __fmaf_rn(s, g, 1.f / 120.f);
-  s = __fmaf_rn(s, g, 1.f / 24.f);
-  s = __fmaf_rn(s, g, 1.f / 6.f);
-  s = __fmaf_rn(s, g, 0.5f);
-  s = __fmaf_rn(s, g, 1.f);
-  return __fmul_rn(s, g);
+__device__ __forceinline__ float2 decay_m1(float2 g) {
+  float2 s = f2(1.f / 40320.f, 1.f / 40320.f);
+  s = __ffma2_rn(s, g, f2(1.f / 5040.f, 1.f / 5040.f));
+  s = __ffma2_rn(s, g, f2(1.f / 720.f, 1.f / 720.f));
+  s = __ffma2_rn(s, g, f2(1.f / 120.f, 1.f / 120.f));
+  s = __ffma2_rn(s, g, f2(1.f / 24.f, 1.f / 24.f));
+  s = __ffma2_rn(s, g, f2(1.f / 6.f, 1.f / 6.f));
+  s = __ffma2_rn(s, g, f2(0.5f, 0.5f));
+  s = __ffma2_rn(s, g, f2(1.f, 1.f));
+  return __fmul2_rn(s, g);
 }
 
-// The gate of one token: a thread keeps one float `w` of it, from which the
-// decay a and the input b come.  PLAIN: w = a.  COMPLEMENT needs a and 1 - a,
-// each with its own relative accuracy: for |g| < 1/2 it keeps e = exp(g) - 1,
-// with a = 1 + e and 1 - a = -e, for the others a (1 - a loses little there);
-// bit `i` of `far` says which.
+// Two gates: a thread keeps one float `w` of each, from which the decay a and
+// the input b come.  PLAIN: w = a.  COMPLEMENT needs a and 1 - a, each with its
+// own relative accuracy: for |g| < 1/2 it keeps e = exp(g) - 1, with a = 1 + e and
+// 1 - a = -e, for the others a (1 - a loses little there); bits `i` and `i + 1` of
+// `far` say which.  Both forms are computed: a branch for each gate costs far more.
 template <int MODE>
-__device__ __forceinline__ float gate_of(float g, unsigned& far, int i) {
-  if (MODE == GDN_GLR_INPUT_PLAIN) return decay(g);
-  const bool is_far = !(fabsf(g) < 0.5f);
-  far |= (unsigned)is_far << i;
-  const float a = decay(g), e = decay_m1(g);  // both: a branch for each token costs far more
-  return is_far ? a : e;
+__device__ __forceinline__ void gates_of(const float (&g)[2], float (&w)[2], unsigned& far,
+                                         int i) {
+  constexpr bool kPlain = MODE == GDN_GLR_INPUT_PLAIN;
+  const float2 both = f2(g[0], g[1]), near2 = kPlain ? decay_near(both) : decay_m1(both);
+  const float near[2] = {near2.x, near2.y};
+#pragma unroll
+  for (int v = 0; v < 2; v++) {
+    const bool is_far = !(fabsf(g[v]) < (kPlain ? 0.125f : 0.5f));
+    if (!kPlain) far |= (unsigned)is_far << (i + v);
+    const float a = decay_far(g[v]);
+    w[v] = is_far ? a : near[v];
+  }
 }
 template <int MODE>
 __device__ __forceinline__ float gate_a(float w, unsigned far, int i) {
@@ -160,6 +183,18 @@ template <int MODE>
 __device__ __forceinline__ float gate_b(float w, unsigned far, int i, float x) {
   if (MODE == GDN_GLR_INPUT_PLAIN) return x;
   return __fmul_rn(far >> i & 1 ? __fsub_rn(1.f, w) : -w, x);
+}
+// The two gates that token t of a chunk starts: its own and, with one channel a
+// thread, the next token's.
+template <int V, class S>
+__device__ __forceinline__ void gate_pair(const S& sg, int t, float (&g)[2]) {
+#pragma unroll
+  for (int j = 0; j < 2; j += V) {
+    float gv[V];
+    widen(sg.get(t + j / V), gv);
+#pragma unroll
+    for (int v = 0; v < V; v++) g[j + v] = gv[v];
+  }
 }
 
 // The zero x of an identity step, whose b is -0 (that of g is +0).
@@ -630,17 +665,18 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(true))
         sg.take();
       }
 #pragma unroll
-      for (int t = 0; t < kGlrChunk; t++) {
-        float xv[V], gv[V];
-        widen(sx.get(t), xv);
-        widen(sg.get(t), gv);
+      for (int i = 0; i < kGlrChunk * V; i += 2) {
+        float gv[2], w[2], xv[V];
+        unsigned far = 0;
+        gate_pair<V>(sg, i / V, gv);
+        gates_of<MODE>(gv, w, far, 0);
 #pragma unroll
-        for (int v = 0; v < V; v++) {
-          unsigned far = 0;
-          const float k = gate_of<MODE>(gv[v], far, 0), a = gate_a<MODE>(k, far, 0);
-          const float b = gate_b<MODE>(k, far, 0, xv[v]);
-          A[t][v] = t ? __fmul_rn(a, A[t - 1][v]) : a;
-          B[t][v] = t ? __fmaf_rn(a, B[t - 1][v], b) : __fmaf_rn(a, 0.f, b);
+        for (int j = 0; j < 2; j++) {
+          const int t = (i + j) / V, v = (i + j) % V;
+          if (v == 0) widen(sx.get(t), xv);
+          const float a = gate_a<MODE>(w[j], far, j), b = gate_b<MODE>(w[j], far, j, xv[v]);
+          A[t][v] = t ? __fmul_rn(a, A[t ? t - 1 : 0][v]) : a;
+          B[t][v] = t ? __fmaf_rn(a, B[t ? t - 1 : 0][v], b) : __fmaf_rn(a, 0.f, b);
         }
       }
     } else {  // only in a cluster's last step: this block's tile is behind the end
@@ -830,18 +866,22 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(false))
         sd.take();
       }
 #pragma unroll
-      for (int t = 0; t < kGlrChunk; t++) {
-        float xv[V], gv[V], dv[V];
-        widen(sx.get(t), xv);
-        widen(sg.get(t), gv);
-        widen(sd.get(t), dv);
+      for (int i = 0; i < kGlrChunk * V; i += 2) {
+        float gv[2], w[2], xv[V], dv[V];
+        gate_pair<V>(sg, i / V, gv);
+        gates_of<MODE>(gv, w, far, i);
 #pragma unroll
-        for (int v = 0; v < V; v++) {
-          ga[t][v] = gate_of<MODE>(gv[v], far, t * V + v);
-          const float a = gate_a<MODE>(ga[t][v], far, t * V + v);
-          const float b = gate_b<MODE>(ga[t][v], far, t * V + v, xv[v]);
-          A[t][v] = t ? __fmul_rn(a, A[t - 1][v]) : a;
-          B[t][v] = t ? __fmaf_rn(a, B[t - 1][v], b) : __fmaf_rn(a, 0.f, b);
+        for (int j = 0; j < 2; j++) {
+          const int t = (i + j) / V, v = (i + j) % V;
+          if (v == 0) {
+            widen(sx.get(t), xv);
+            widen(sd.get(t), dv);
+          }
+          ga[t][v] = w[j];
+          const float a = gate_a<MODE>(w[j], far, i + j);
+          const float b = gate_b<MODE>(w[j], far, i + j, xv[v]);
+          A[t][v] = t ? __fmul_rn(a, A[t ? t - 1 : 0][v]) : a;
+          B[t][v] = t ? __fmaf_rn(a, B[t ? t - 1 : 0][v], b) : __fmaf_rn(a, 0.f, b);
           M[v] = t ? __fmaf_rn(A[t][v], dv[v], M[v]) : __fmul_rn(a, dv[v]);
         }
       }
@@ -939,17 +979,21 @@ __global__ void __launch_bounds__(kGlrShortThreads) k_glr_short_forward(const Gl
     const int have = min(kGlrChunk, L - t0);
     OUT* out = h + (int64_t)t0 * p.ldh;
 #pragma unroll
-    for (int t = 0; t < kGlrChunk; t++) {
-      float xv[1], gv[1];
-      widen(sx.get(t), xv);
-      widen(sg.get(t), gv);
+    for (int i = 0; i < kGlrChunk; i += 2) {
+      float gv[2], w[2], xv[1];
       unsigned far = 0;
-      const float k = gate_of<MODE>(gv[0], far, 0), a = gate_a<MODE>(k, far, 0);
-      const float b = gate_b<MODE>(k, far, 0, xv[0]);
-      A = t ? __fmul_rn(a, A) : a;
-      B = t ? __fmaf_rn(a, B, b) : __fmaf_rn(a, 0.f, b);
-      hv[0] = __fmaf_rn(A, Hm, B);
-      if (t < have) put(row_at(out, p.ldh, t), hv);
+      gate_pair<1>(sg, i, gv);
+      gates_of<MODE>(gv, w, far, 0);
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        const int t = i + j;
+        widen(sx.get(t), xv);
+        const float a = gate_a<MODE>(w[j], far, j), b = gate_b<MODE>(w[j], far, j, xv[0]);
+        A = t ? __fmul_rn(a, A) : a;
+        B = t ? __fmaf_rn(a, B, b) : __fmaf_rn(a, 0.f, b);
+        hv[0] = __fmaf_rn(A, Hm, B);
+        if (t < have) put(row_at(out, p.ldh, t), hv);
+      }
     }
     H[0] = hv[0];
   }
@@ -998,15 +1042,19 @@ __global__ void __launch_bounds__(kGlrShortThreads) k_glr_short_backward(const G
     sg.take();
     far = 0;
 #pragma unroll
-    for (int t = 0; t < kGlrChunk; t++) {
-      float xv[1], gv[1];
-      widen(sx.get(t), xv);
-      widen(sg.get(t), gv);
-      w[t] = gate_of<MODE>(gv[0], far, t);
-      const float a = gate_a<MODE>(w[t], far, t);
-      const float b = gate_b<MODE>(w[t], far, t, xv[0]);
-      A[t] = t ? __fmul_rn(a, A[t - 1]) : a;
-      B[t] = t ? __fmaf_rn(a, B[t - 1], b) : __fmaf_rn(a, 0.f, b);
+    for (int i = 0; i < kGlrChunk; i += 2) {
+      float gv[2], k[2], xv[1];
+      gate_pair<1>(sg, i, gv);
+      gates_of<MODE>(gv, k, far, i);
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        const int t = i + j;
+        widen(sx.get(t), xv);
+        w[t] = k[j];
+        const float a = gate_a<MODE>(k[j], far, t), b = gate_b<MODE>(k[j], far, t, xv[0]);
+        A[t] = t ? __fmul_rn(a, A[t ? t - 1 : 0]) : a;
+        B[t] = t ? __fmaf_rn(a, B[t ? t - 1 : 0], b) : __fmaf_rn(a, 0.f, b);
+      }
     }
   };
   for (int tile = (L - 1) / kGlrTile; L > 0 && tile >= 0; tile--) {
@@ -1095,13 +1143,15 @@ __global__ void __launch_bounds__(kGlrStepThreads) k_glr_step(const GlrArgs p) {
   const bool full = pos == kGlrChunk - 1;
   if (threadIdx.x == 0) p.st.pos[slot] = full ? 0 : pos + 1;
   for (int ch = threadIdx.x * V; ch < p.D; ch += blockDim.x * V) {
-    float hv[V];
+    float hv[V], w[2];
+    const float pair[2] = {gv[0], gv[V - 1]};
+    unsigned far = 0;
+    gates_of<MODE>(pair, w, far, 0);
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      unsigned far = 0;
-      const float wv = gate_of<MODE>(gv[v], far, 0), a = gate_a<MODE>(wv, far, 0);
+      const float a = gate_a<MODE>(w[v], far, v);
       A[v] = __fmul_rn(a, pos ? A[v] : 1.f);
-      B[v] = __fmaf_rn(a, pos ? B[v] : 0.f, gate_b<MODE>(wv, far, 0, xv[v]));
+      B[v] = __fmaf_rn(a, pos ? B[v] : 0.f, gate_b<MODE>(w[v], far, v, xv[v]));
       hv[v] = __fmaf_rn(A[v], H[v], B[v]);
       if (full) {
         A[v] = 1.f;

@@ -1,0 +1,100 @@
+"""GPU checks of the gated linear recurrence at the edges of what its header
+allows: the gates themselves, slow gates, batches of very unequal sequences,
+gates that grow, invalid cu_seqlens and what lies behind a sequence's end.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import glr
+from rl_train_numerics_b200 import workloads as W
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    from rl_train_numerics_b200 import _abi
+    return _abi
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def draw(lens, D, seed, dt=BF, gt=F32):
+    """x, g, d_h [T, D], h0, ds [N, D] and cu_seqlens, on the GPU."""
+    r = torch.Generator().manual_seed(seed)
+    T, N = sum(lens), len(lens)
+    rand = lambda *s: torch.randn(s, generator=r)  # noqa: E731
+    g = -torch.nn.functional.softplus(rand(T, D))
+    return (rand(T, D).to(dt).cuda(), g.to(gt).cuda(), rand(T, D).to(dt).cuda(),
+            rand(N, D).cuda(), rand(N, D).cuda(), W.cu_seqlens_of(lens, "cuda"))
+
+
+def close(got, want, bound, what=""):
+    err = np.abs(f64(got) - want)
+    assert (err <= bound).all(), (what, float((err / bound).max()))
+
+
+def ok(gdn, error):
+    assert gdn.check_error(error) == 0
+
+
+@pytest.mark.parametrize("complement", [False, True])
+@pytest.mark.parametrize("lens,D", [([1], 4096), ([1], 4095), ([1] * 4, 4096), (None, 4096),
+                                    (None, 4095)])
+def test_a_gate_is_as_exact_as_stated(gdn, lens, D, complement):
+    """One token with x = 0 from h0 = 1 returns its decay: A = a, B = 0, h = fma(a, 1, 0).
+    Tiles, rows no tensor map describes, short sequences and the decode step (None)."""
+    r = np.random.default_rng(5)
+    size = 10.0 ** r.uniform(-7, 2, (4, D))
+    size[:, ::3] = r.uniform(0, 0.6, size[:, ::3].shape)    # slow gates, and the forms' borders
+    g = torch.from_numpy(-size).float()
+    g[:, 1::7] = -g[:, 1::7].clamp(min=-0.45)               # some of them growing
+    g = g[:len(lens) if lens else 4].cuda().contiguous()
+    N = g.shape[0]
+    x = torch.zeros_like(g)
+    one = torch.ones((N, D), device="cuda")
+    if lens:
+        a, fin, _, err = gdn.glr_forward(x, g, W.cu_seqlens_of(lens, "cuda"), h0=one,
+                                         complement=complement)
+        ok(gdn, err)
+        assert torch.equal(a, fin)
+    else:
+        state = gdn.GlrDecodeState(N, D)
+        state.h.copy_(one)
+        a = gdn.glr_decode_step(state, x, g, complement=complement)
+        ok(gdn, state.error)
+    want = np.exp(f64(g))
+    bound = want * glr.decay_bound(f64(g), complement) * 1.01
+    bound = np.where(want < 2.0 ** -125, want, bound)       # a below 2^-126 counts as 0
+    close(a, want, bound)
+    if not complement:      # half a step towards 0, where a state lives long
+        slow = (f64(g) < 0) & (f64(g) > -0.125)
+        err = np.abs(f64(a) - want) / want
+        assert slow.sum() > 100 and err[slow].max() <= 0.8 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("complement", [False, True])
+def test_slow_gates_over_a_long_sequence(gdn, complement):
+    """States that live for 10^2 to 10^5 tokens: the sums take a gate's error up as often."""
+    T, D = 30000, 8
+    r = torch.Generator().manual_seed(9)
+    x = (1 + 0.5 * torch.randn((T, D), generator=r)).cuda()
+    rate = torch.tensor([1e-2, 1e-3, 3e-4, 1e-4, 7e-5, 3e-5, 1.1e-5, 0.06])
+    g = (-rate).expand(T, D).contiguous().cuda()
+    dh = torch.randn((T, D), generator=r).cuda()
+    cu = W.cu_seqlens_of([T], "cuda")
+    h, fin, carry, err = gdn.glr_forward(x, g, cu, complement=complement, want_carry=True)
+    ok(gdn, err)
+    args = (f64(x), f64(g), [T])
+    close(h, glr.forward(*args, None, complement)[0],
+          glr.forward_bound(*args, None, complement)[0], "h")
+    grads, err = gdn.glr_backward(x, g, cu, carry, dh, complement=complement)
+    ok(gdn, err)
+    want = glr.backward(*args, f64(dh), complement=complement)
+    bound = glr.backward_bound(*args, f64(dh), complement=complement)
+    for got, w, b in zip((grads["dx"], grads["dg"], grads["dh0"]), want, bound):
+        close(got, w, b)
