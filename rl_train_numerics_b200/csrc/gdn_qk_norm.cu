@@ -110,6 +110,14 @@ __device__ __forceinline__ float2 angle(int pos, uint64_t f) {
   return quarter & 2 ? f2(-x, -y) : f2(x, y);
 }
 
+// (sum x^2 [/ d] + eps)^(-1/2), off by at most two units in the last place: the
+// correctly rounded function takes 66 us forward and 107 backward at 16384 x (32 +
+// 8) rotated heads (59 and 100), and would take 3 U (U = 2^-24) off the 17 U that
+// bound an fp32 y.
+__device__ __forceinline__ float inverse_norm(float sum, const QkArgs& p) {
+  return rsqrtf(__fmaf_rn(sum, p.inv_m, p.eps));
+}
+
 // Where a lane stands in its head: its pieces' first channels, and the first of
 // its angles (-1: its channels are not rotated).
 struct QkLane {
@@ -300,7 +308,7 @@ __global__ void __launch_bounds__(kQkThreads, qk_forward_blocks(ROT, sizeof(IN))
       Eight n;
       widen4(ra[i], n.v);
       widen4(rb[i], n.v + 2);
-      scale8(n, rsqrtf(__fmaf_rn(dot8<D>(n, n), p.inv_m, p.eps)));
+      scale8(n, inverse_norm(dot8<D>(n, n), p));
       if (sd.w) times8(n, w);
       rotate8<ROT>(n, l, turn);
       if (write) {
@@ -390,7 +398,7 @@ __global__ void __launch_bounds__(kQkThreads, qk_backward_blocks(ROT, D))
       widen4(cur.ga[i], e.v);
       widen4(cur.gb[i], e.v + 2);
       rotate8<ROT>(e, l, turn);
-      const float r = rsqrtf(__fmaf_rn(dot8<D>(n, n), p.inv_m, p.eps));
+      const float r = inverse_norm(dot8<D>(n, n), p);
       if (sd.w) {
         const float2 rr = f2(r, r);
 #pragma unroll
