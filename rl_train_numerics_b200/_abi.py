@@ -636,7 +636,8 @@ def qk_norm_backward(q, k, d_oq, d_ok, *, norm: str = "l2", eps: float = 1e-6, w
     """gdn_qk_norm_backward: q, k and the options of the forward; d_oq, d_ok of
     one dtype (bf16 or fp32, the fp32 of backward()'s dq and dk for one).  Returns
     a dict of dq, dk (the dtype of q and k) and dwq, dwk [d] fp32 (None without
-    the weight or want_dw).  Pass ``grads`` (the same dict) to reuse buffers."""
+    the weight or want_dw).  Pass ``grads`` (such a dict) to reuse its buffers; what
+    it lacks is allocated as without it."""
     c, dt, (T, Hq, Hk, d), head, tail = _qk_call("gdn_qk_norm_backward", q, k, norm, wq, wk,
                                                  positions, inv_freq, stream)
     c.need((q is None) == (d_oq is None) and (k is None) == (d_ok is None),
@@ -650,11 +651,11 @@ def qk_norm_backward(q, k, d_oq, d_ok, *, norm: str = "l2", eps: float = 1e-6, w
             res["d" + s] = None
             continue
         gin += [*c.rows(g, "d_o" + s, (T, H, d), gdt)]
-        given = grads["d" + s] if grads is not None else None
+        given = grads.get("d" + s) if grads is not None else None
         res["d" + s], *at = c.out_rows(given, "d" + s, (T, H, d), dt)
         gout += at
     for s, w in (("q", wq), ("k", wk)):
-        given = grads["dw" + s] if grads is not None and w is not None and want_dw else None
+        given = grads.get("dw" + s) if grads is not None and w is not None and want_dw else None
         res["dw" + s], at = c.out_full(given, w is not None and want_dw, "dw" + s, (d,),
                                        torch.float32)
         gout.append(at)
@@ -771,7 +772,8 @@ def glr_backward(x, g, cu_seqlens, carry, d_h, *, n_seqs: Optional[int] = None, 
     """gdn_glr_backward: x, g, cu_seqlens and options of the forward that wrote
     ``carry``; d_h [T, D] (bf16 or fp32).  Returns (grads, error word); grads is
     a dict of dx, dg [T, D] (the dtypes of x and g) and dh0 [N, D] fp32 (None
-    unless want_dh0).  Pass ``grads`` (the same dict) to reuse buffers."""
+    unless want_dh0).  Pass ``grads`` (such a dict) to reuse its buffers; what it
+    lacks is allocated and put into it."""
     c = _Call("gdn_glr_backward", x, stream)
     c.need(x.dim() == 2 and g.dim() == 2, "x, g must be [tokens, channels]")
     T, D = x.shape
@@ -780,13 +782,12 @@ def glr_backward(x, g, cu_seqlens, carry, d_h, *, n_seqs: Optional[int] = None, 
     dhp, lddh = c.rows(d_h, "d_h", (T, D))
     c.need(carry is not None, "carry is the forward's (want_carry=True)")
     car = c.full(carry, "carry", (glr_carry_rows(N, T), D), torch.float32)
-    given = grads if grads is not None else {}
-    dx, dxp, lddx = c.out_rows(given.get("dx"), "dx", (T, D), x.dtype)
-    dg, dgp, lddg = c.out_rows(given.get("dg"), "dg", (T, D), g.dtype)
-    dh0, dhp0 = c.out_full(given.get("dh0"), want_dh0 and grads is None, "dh0", (N, D),
-                           torch.float32)
     if grads is None:
-        grads = {"dx": dx, "dg": dg, "dh0": dh0}
+        grads = {}
+    dx, dxp, lddx = c.out_rows(grads.get("dx"), "dx", (T, D), x.dtype)
+    dg, dgp, lddg = c.out_rows(grads.get("dg"), "dg", (T, D), g.dtype)
+    dh0, dhp0 = c.out_full(grads.get("dh0"), want_dh0, "dh0", (N, D), torch.float32)
+    grads.update(dx=dx, dg=dg, dh0=dh0)
     error, err = c.out_full(error, True, "error", (1,), torch.int32)
     c.run(lib.gdn_glr_backward, *ins, cu, N, T, D, _glr_mode(complement), car, dhp, lddh,
           _dtype_code(d_h), c.full(ds_final, "ds_final", (N, D), torch.float32), dxp, lddx, dgp,

@@ -98,3 +98,18 @@ def test_slow_gates_over_a_long_sequence(gdn, complement):
     bound = glr.backward_bound(*args, f64(dh), complement=complement)
     for got, w, b in zip((grads["dx"], grads["dg"], grads["dh0"]), want, bound):
         close(got, w, b)
+
+
+@pytest.mark.parametrize("have", [(), ("dx",), ("dg",), ("dh0",), ("dx", "dg")])
+def test_gradient_buffers_that_are_not_given_are_made(gdn, have):
+    x, g, dh, h0, ds, cu = draw([20, 5], 64, 12)
+    _, _, carry, _ = gdn.glr_forward(x, g, cu, h0=h0, want_carry=True)
+    want, _ = gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds)
+    buf = {k: torch.empty_like(want[k]) for k in have}
+    mine = dict(buf)
+    got, _ = gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds, grads=buf)
+    assert got is buf and set(got) == {"dx", "dg", "dh0"}
+    assert all(got[k] is mine[k] for k in have)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    got, _ = gdn.glr_backward(x, g, cu, carry, dh, grads={"dh0": None}, want_dh0=False)
+    assert got["dh0"] is None and got["dg"] is not None
