@@ -209,6 +209,7 @@ struct GlrArgs {
   int N;
   int T, D, slabs, stages;
   bool longest_first;  // tile kernels: the grid's order of the sequences
+  int longer;  // > 0: tile kernels take the sequences of more tokens, short ones the others
   const float* h0;  // forward
   void* h;
   int ldh;
@@ -263,6 +264,26 @@ __device__ __forceinline__ bool glr_seq_by_length(const GlrArgs& p, int r, int& 
   return (zero == 0) & (total == p.T) & (start >= 0) & (stop >= start) & (stop <= p.T);
 }
 
+// The sequence of more than p.longer tokens of which token j * p.longer is the first
+// that is a multiple of p.longer; false when there is none.  So T / p.longer blocks
+// of a slab find all of them, wherever they are.  A warp looks at 32 edges at a
+// time; any cu_seqlens keep its reads inside.
+__device__ __forceinline__ bool glr_seq_longer(const GlrArgs& p, int j, int& n, int& start,
+                                               int& length) {
+  const int token = j * p.longer;
+  int width = p.N;
+  n = 0;
+  while (width > 1) {  // the sequence is one of n .. n + width - 1
+    const int step = (width + 31) / 32, i = (threadIdx.x & 31) * step;
+    const unsigned m = __ballot_sync(kFull, i < width && p.cu[n + i] <= token);
+    const int first = m ? (31 - __clz(m)) * step : 0;
+    n += first;
+    width = min(step, width - first);
+  }
+  return glr_seq(p, n, start, length) && length > p.longer && start <= token &&
+         token - start < p.longer;
+}
+
 // Slot of row n, or -1 when it is out of range or an earlier row has it too.
 // Any threads call the first form, the whole block the second.
 __device__ __forceinline__ int glr_slot(const int32_t* slot_idx, int n, int n_slots) {
@@ -315,10 +336,16 @@ __device__ __forceinline__ bool glr_place(const GlrArgs& p, GlrPlace& at) {
   const int unit = blockIdx.x / at.cs;
   const int turn = unit / p.slabs;
   at.slab = unit % p.slabs;
-  glr_report(p);
+  if (p.longer == 0) {
+    glr_report(p);
+  } else if (unit == (int)(gridDim.x / at.cs) - 1) {
+    pdl_wait();  // no sequence is left for the last blocks, which keep the grid from
+    return false;  // ending before that of the short kernel
+  }
   at.n = turn;
-  const bool valid = p.longest_first ? glr_seq_by_length(p, turn, at.n, at.start, at.L)
-                                     : glr_seq(p, at.n, at.start, at.L);
+  const bool valid = p.longer > 0       ? glr_seq_longer(p, turn, at.n, at.start, at.L)
+                     : p.longest_first ? glr_seq_by_length(p, turn, at.n, at.start, at.L)
+                                       : glr_seq(p, at.n, at.start, at.L);
   if (!valid) return false;  // the same for a whole cluster
   at.c = threadIdx.x / (kGlrSlab / V);
   at.col = threadIdx.x % (kGlrSlab / V) * V;
@@ -947,12 +974,20 @@ __global__ void __launch_bounds__((kGlrBlock<V>), glr_blocks<V>(false))
 // spends on a sequence of a few tokens.
 constexpr int kGlrShortThreads = 128;
 
+// Sequence n of a block of the short kernels; false when it is not for it.  Where
+// the call has longer ones (p.longer), their tile kernel is the next and shares the
+// device with this one.
+__device__ __forceinline__ bool glr_short_seq(const GlrArgs& p, int n, int& start, int& L) {
+  if (p.longer > 0) pdl_trigger();
+  glr_report(p);
+  return glr_seq(p, n, start, L) && (p.longer == 0 || L <= p.longer);
+}
+
 template <class IN, class G, class OUT, int MODE>
 __global__ void __launch_bounds__(kGlrShortThreads) k_glr_short_forward(const GlrArgs p) {
   const int n = blockIdx.x / p.slabs, ch = blockIdx.x % p.slabs * kGlrShortThreads + threadIdx.x;
-  glr_report(p);
   int start, L;
-  if (!glr_seq(p, n, start, L)) return;
+  if (!glr_short_seq(p, n, start, L)) return;
   const bool live = ch < p.D;
   const IN* x = static_cast<const IN*>(p.x) + (int64_t)start * p.ldx + ch;
   const G* g = static_cast<const G*>(p.g) + (int64_t)start * p.ldg + ch;
@@ -1019,9 +1054,8 @@ template <class IN, class G, class OUT, int MODE>
 __global__ void __launch_bounds__(kGlrShortThreads) k_glr_short_backward(const GlrArgs p) {
   __shared__ float enter[kGlrChunks][kGlrShortThreads];  // a thread's own column
   const int n = blockIdx.x / p.slabs, ch = blockIdx.x % p.slabs * kGlrShortThreads + threadIdx.x;
-  glr_report(p);
   int start, L;
-  if (!glr_seq(p, n, start, L)) return;
+  if (!glr_short_seq(p, n, start, L)) return;
   if (ch >= p.D) return;
   const IN* x = static_cast<const IN*>(p.x) + (int64_t)start * p.ldx + ch;
   const G* g = static_cast<const G*>(p.g) + (int64_t)start * p.ldg + ch;
@@ -1211,11 +1245,15 @@ static GlrShape glr_shape(const GlrArgs& p, size_t stage, int most, bool backwar
     const int64_t n = kSmem / (kBlock + maps(cs) + 2 * stage);
     return kSms * (n < most ? n : most);
   };
-  const int64_t units = (int64_t)p.N * p.slabs;
-  const int max_cluster = backward ? 4 : 8;
+  // (there may be one sequence longer than p.longer; two blocks for each: 4 take 269
+  // us where 2 take 402 above, but 8 such sequences of 2040 tokens 86 forward, not
+  // 68, and where there are none the clusters to start are the cost)
+  const int seqs = p.longer > 0 ? 1 : p.N;
+  const int64_t units = (int64_t)seqs * p.slabs;
+  const int max_cluster = p.longer > 0 ? 2 : backward ? 4 : 8;
   GlrShape sh{1, 0, false, 0};
   while (sh.cs < max_cluster && units * 2 * sh.cs <= places(2 * sh.cs) &&
-         p.T > (int64_t)p.N * kGlrTile * sh.cs)
+         p.T > (int64_t)seqs * kGlrTile * sh.cs)
     sh.cs *= 2;
   // Sequences of unequal length keep the device waiting for the longest: two
   // blocks for each then gain more than a second wave of blocks costs (10240
@@ -1224,16 +1262,17 @@ static GlrShape glr_shape(const GlrArgs& p, size_t stage, int most, bool backwar
   // backward from a few more units on (20000 x 2048 in 9, uneven: 104 against 133
   // us, 18432 in 9 equal ones: 94 against 104; the forward the same within 2 us).
   const int waves = backward && stage > 0 ? 4 : most;
-  if (sh.cs == 1 && p.N > 1 && units <= waves * kSms && p.T > (int64_t)p.N * kGlrTile) sh.cs = 2;
+  if (sh.cs == 1 && seqs > 1 && units <= waves * kSms && p.T > (int64_t)seqs * kGlrTile)
+    sh.cs = 2;
   int64_t here = (units * sh.cs + kSms - 1) / kSms;  // blocks of a multiprocessor
-  here = here < most ? here : most;
+  here = here < most && p.longer == 0 ? here : most;
   if (stage > 0) {
     const size_t fixed = kBlock + maps(sh.cs), least = backward && sh.cs > 1 ? 3 : 2;
     while (here > 1 && kSmem / here < fixed + least * stage) here--;
     sh.stages = (int)((kSmem / here - fixed) / stage);
     if (sh.stages > kGlrMaxStages) sh.stages = kGlrMaxStages;
   }
-  sh.longest_first = p.N > 1 && p.N <= kGlrOrder && units * sh.cs > here * kSms;
+  sh.longest_first = seqs > 1 && seqs <= kGlrOrder && units * sh.cs > here * kSms;
   sh.smem = sh.stages * stage + maps(sh.cs);
   return sh;
 }
@@ -1248,17 +1287,20 @@ static cudaError_t glr_run(K kernel, int threads, size_t stage, int most, bool b
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        227 * 1024 - (int)kGlrStatic);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)sh.cs;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)sh.cs;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // behind the short kernel
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.N * (unsigned)p.slabs * (unsigned)sh.cs);
+  const unsigned turns = p.longer > 0 ? (unsigned)((p.T + p.longer - 1) / p.longer) : p.N;
+  cfg.gridDim = dim3((turns * (unsigned)p.slabs + (p.longer > 0)) * (unsigned)sh.cs);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = sh.smem;
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.longer > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, box);
 }
 
@@ -1279,27 +1321,7 @@ static bool glr_encode(CUtensorMap* map, const void* base, int64_t tokens, int D
 }
 
 template <class IN, class G, class OUT, int MODE>
-static cudaError_t glr_launch(GlrOp op, GlrArgs& p, bool pairs, cudaStream_t st) {
-  p.slabs = (p.D + kGlrSlab - 1) / kGlrSlab;
-  if (op == kGlrStep) {
-    if (pairs)
-      k_glr_step<IN, G, OUT, 2, MODE><<<(unsigned)p.N, glr_step_threads<2>(p.D), 0, st>>>(p);
-    else
-      k_glr_step<IN, G, OUT, 1, MODE><<<(unsigned)p.N, glr_step_threads<1>(p.D), 0, st>>>(p);
-    return cudaGetLastError();
-  }
-  // Sequences of up to 64 tokens on average, and more of them than one wave of
-  // tile blocks takes: 64 sequences of 4096 channels, forward and backward, 300
-  // tokens: 35 us (tiles: 130), 4096: 127 (161), 8192: 238 (207).
-  if (p.T <= (int64_t)64 * p.N && (int64_t)p.N * p.slabs > 3 * 148) {
-    p.slabs = (p.D + kGlrShortThreads - 1) / kGlrShortThreads;
-    const unsigned blocks = (unsigned)p.N * (unsigned)p.slabs;
-    if (op == kGlrFwd)
-      k_glr_short_forward<IN, G, OUT, MODE><<<blocks, kGlrShortThreads, 0, st>>>(p);
-    else
-      k_glr_short_backward<IN, G, OUT, MODE><<<blocks, kGlrShortThreads, 0, st>>>(p);
-    return cudaGetLastError();
-  }
+static cudaError_t glr_tiles(GlrOp op, GlrArgs& p, bool pairs, cudaStream_t st) {
   GlrBoxes box{};
   // pairs: the rows that are written take two elements at a time
   const bool staged = pairs && p.T > 0 && glr_encode<IN>(&box.x, p.x, p.T, p.D, p.ldx) &&
@@ -1317,6 +1339,52 @@ static cudaError_t glr_launch(GlrOp op, GlrArgs& p, bool pairs, cudaStream_t st)
                    sizeof(GlrBackwardStage<IN, G, OUT>), glr_blocks<2>(false), true, p, box, st);
   return glr_run(k_glr_backward<IN, G, OUT, 1, MODE, false>, kGlrBlock<1>, 0,
                  glr_blocks<1>(false), true, p, box, st);
+}
+
+template <class IN, class G, class OUT, int MODE>
+static cudaError_t glr_launch(GlrOp op, GlrArgs& p, bool pairs, cudaStream_t st) {
+  p.slabs = (p.D + kGlrSlab - 1) / kGlrSlab;
+  if (op == kGlrStep) {
+    if (pairs)
+      k_glr_step<IN, G, OUT, 2, MODE><<<(unsigned)p.N, glr_step_threads<2>(p.D), 0, st>>>(p);
+    else
+      k_glr_step<IN, G, OUT, 1, MODE><<<(unsigned)p.N, glr_step_threads<1>(p.D), 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  // Sequences of up to 64 tokens on average, and more of them than one wave of
+  // tile blocks takes: 64 sequences of 4096 channels, forward and backward, 300
+  // tokens: 35 us (tiles: 130), 4096: 132 (161), 8192: 238 (207).
+  if (p.T > (int64_t)64 * p.N || (int64_t)p.N * p.slabs <= 3 * 148)
+    return glr_tiles<IN, G, OUT, MODE>(op, p, pairs, st);
+  // The average says nothing of the longest, and a thread that walks thousands of
+  // tokens alone would keep the device waiting: sequences of more than p.longer
+  // tokens go to tile blocks, which share the device with the short kernel's.  63
+  // sequences of one token and one of 3968, of 4096 channels: 43 us forward and 55
+  // backward (219 and 700 by the short kernel alone; the long one alone 29 and 41);
+  // 600 tokens in 999 and 60000 in one, 2048 channels: 402 and 512 (3052 and 10093).
+  //
+  // Since only the device knows the lengths, there are blocks for each sequence
+  // that might be so long, T / p.longer of them, and those that find none cost
+  // some time: 1000 sequences of 60 tokens of 2048 channels 203 and 395 us (without
+  // them 191 and 383), 64 of 64 tokens of 4096 33 and 61 (31 and 57).  That grows
+  // with their number, so they are kept to some for the work there is.  Up to the
+  // least length it is worth no second launch (1024 tokens forward: 66 us, 512
+  // backward: 97), and calls of so few tokens in all have none.
+  const int least = op == kGlrFwd ? 1024 : 512;
+  const int64_t turns = 1 + (512 + (int64_t)p.T * p.D / 65536) / p.slabs;
+  const int64_t share = (p.T + turns - 1) / turns;
+  p.longer = share > least ? (int)share : least;
+  if (p.T <= p.longer) p.longer = 0;
+  p.slabs = (p.D + kGlrShortThreads - 1) / kGlrShortThreads;
+  const unsigned blocks = (unsigned)p.N * (unsigned)p.slabs;
+  if (op == kGlrFwd)
+    k_glr_short_forward<IN, G, OUT, MODE><<<blocks, kGlrShortThreads, 0, st>>>(p);
+  else
+    k_glr_short_backward<IN, G, OUT, MODE><<<blocks, kGlrShortThreads, 0, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.longer == 0) return e;
+  p.slabs = (p.D + kGlrSlab - 1) / kGlrSlab;
+  return glr_tiles<IN, G, OUT, MODE>(op, p, pairs, st);
 }
 
 template <class IN, class G, class OUT>

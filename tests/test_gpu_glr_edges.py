@@ -113,3 +113,121 @@ def test_gradient_buffers_that_are_not_given_are_made(gdn, have):
     assert all(torch.equal(got[k], want[k]) for k in want)
     got, _ = gdn.glr_backward(x, g, cu, carry, dh, grads={"dh0": None}, want_dh0=False)
     assert got["dh0"] is None and got["dg"] is not None
+
+
+UNEQUAL = {  # mostly short sequences, some far longer: both kinds of kernels in one call
+    "one": ([1] * 40 + [3600] + [2] * 59, 512),
+    "borders": ([512, 3] * 2 + [513, 1024, 0, 1025, 511] + [1] * 80, 512),
+    "first and last": ([1500] + [0] * 60 + [7] * 9 + [2100], 1024),
+    "rows off 16 bytes": ([5] * 30 + [2000, 0, 1300] + [9] * 70, 257),
+    "many": (([0, 1, 3, 2] * 300 + [3000]) * 3 + [600, 1030] + [4] * 200, 64),
+}
+
+
+@pytest.mark.parametrize("name", list(UNEQUAL))
+@pytest.mark.parametrize("complement", [False, True])
+def test_unequal_sequences(gdn, name, complement):
+    """Bits of sequences alone, final and decode states, and the oracle."""
+    lens, D = UNEQUAL[name]
+    N = len(lens)
+    x, g, dh, h0, ds, cu = draw(lens, D, 81)
+    slots = torch.arange(N, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    state = gdn.GlrDecodeState(N, D)
+    kw = dict(complement=complement)
+    fill = torch.full((sum(lens), D), float("nan"), dtype=BF, device="cuda")
+    h, fin, carry, err = gdn.glr_forward(x, g, cu, h0=h0, state=state, slot_idx=slots, h=fill,
+                                         want_carry=True, **kw)
+    ok(gdn, err)
+    ok(gdn, state.error)
+    assert state.pos.flip(0).tolist() == [n % 16 for n in lens]
+    grads, err = gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds, **kw)
+    ok(gdn, err)
+    edges = cu.tolist()
+    order = sorted(range(N), key=lambda n: -lens[n])
+    for n in order[:6] + order[-2:] + [order[N // 2]]:
+        rows = slice(edges[n], edges[n + 1])
+        one = gdn.GlrDecodeState(1, D)
+        c = W.cu_seqlens_of([lens[n]], "cuda")
+        h1, f1, c1, _ = gdn.glr_forward(x[rows], g[rows], c, h0=h0[n:n + 1], state=one,
+                                        want_carry=True, **kw)
+        g1, _ = gdn.glr_backward(x[rows], g[rows], c, c1, dh[rows], ds_final=ds[n:n + 1], **kw)
+        assert torch.equal(h1, h[rows]) and torch.equal(f1[0], fin[n]), n
+        assert torch.equal(g1["dx"], grads["dx"][rows]) and torch.equal(g1["dg"],
+                                                                        grads["dg"][rows]), n
+        assert torch.equal(g1["dh0"][0], grads["dh0"][n]), n
+        assert all(torch.equal(a[0], b[N - 1 - n]) for a, b in zip(one.tensors(),
+                                                                   state.tensors())), n
+    ch = [0, D - 1]
+    args = (f64(x[:, ch]), f64(g[:, ch]), lens)
+    init = f64(h0[:, ch])
+    want, wfin = glr.forward(*args, init, complement)
+    bound, bfin = glr.forward_bound(*args, init, complement)
+    close(h[:, ch], want, bound + 2.0 ** -8 * (np.abs(want) + bound), "h")
+    close(fin[:, ch], wfin, bfin, "s_final")
+    want = glr.backward(*args, f64(dh[:, ch]), init, f64(ds[:, ch]), complement)
+    bound = glr.backward_bound(*args, f64(dh[:, ch]), init, f64(ds[:, ch]), complement)
+    close(grads["dx"][:, ch], want[0], bound[0] + 2.0 ** -8 * (np.abs(want[0]) + bound[0]), "dx")
+    close(grads["dg"][:, ch], want[1], bound[1], "dg")
+    close(grads["dh0"][:, ch], want[2], bound[2], "dh0")
+
+
+def test_unequal_sequences_captured_and_on_a_side_stream(gdn):
+    lens, D = UNEQUAL["first and last"]
+    x, g, dh, h0, ds, cu = draw(lens, D, 82)
+
+    def both():
+        h, fin, carry, _ = gdn.glr_forward(x, g, cu, h0=h0, want_carry=True)
+        grads, err = gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds)
+        return h, fin, grads["dx"], grads["dg"], grads["dh0"], err, h.float() + 1
+
+    want = both()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            got = both()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both()
+    x.neg_()
+    dh.mul_(2)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(out, both()))
+
+
+def test_a_long_sequence_among_short_ones_is_not_walked_by_one_thread(gdn):
+    """Within four times the same sequence alone (1.5 measured; a walk by one thread for
+    each channel takes 8 times as long forward and 17 backward)."""
+    D, L = 4096, 3968
+    x, g, dh, h0, ds, cu = draw([1] * 40 + [L] + [1] * 23, D, 83)
+
+    def best(x, g, dh, h0, ds, cu):
+        _, _, carry, err = gdn.glr_forward(x, g, cu, h0=h0, want_carry=True)
+        grads, _ = gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds)
+        kw = dict(h=dh.clone(), s_final=ds.clone(), error=err)
+        calls = (lambda: gdn.glr_forward(x, g, cu, h0=h0, carry=carry, **kw),
+                 lambda: gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds, grads=grads,
+                                          error=err))
+        out = []
+        for call in calls:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                for _ in range(5):
+                    call()
+            times = []
+            for _ in range(7):
+                a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+                a.record()
+                graph.replay()
+                b.record()
+                b.synchronize()
+                times.append(a.elapsed_time(b))
+            out.append(min(times))
+        return out
+
+    among = best(x, g, dh, h0, ds, cu)
+    rows = slice(40, 40 + L)
+    alone = best(x[rows], g[rows], dh[rows], h0[:1], ds[:1], W.cu_seqlens_of([L], "cuda"))
+    assert among[0] < 4 * alone[0] and among[1] < 4 * alone[1], (among, alone)
