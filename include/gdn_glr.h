@@ -29,6 +29,10 @@
  * contiguous fp32 arrays [rows, D] need only the alignment of their elements
  * (16 bytes for a decode state).  Rows that start on 16 bytes are the fast ones.
  * g may be -inf; it must not be NaN or +inf.  An a below 2^-126 counts as 0.
+ * Gates may grow (g > 0) as long as A stays in fp32's range: the sum of g over
+ * the first tokens of a chunk, up to any of them, stays below 88 (16 gates of
+ * 5.5).  Beyond that A is infinite, and h is NaN where the state that entered
+ * the chunk is 0, or after a reset in the same chunk.
  * D is any size from 1 to 2^24, total_tokens up to 2^31 - 4097, strides up to
  * 2^27 elements, n_seqs ceil(D / 32) up to 2^28 - 1.
  */

@@ -744,7 +744,8 @@ def glr_forward(x, g, cu_seqlens, *, n_seqs: Optional[int] = None, h0=None,
                 carry=None, want_carry: bool = False, error=None, stream=None):
     """gdn_glr_forward: h_t = exp(g_t) h_{t-1} + x_t for every channel of packed
     sequences (complement: + (1 - exp(g_t)) x_t).  x, g [T, D], rows may be
-    strided; h0, s_final [N, D] fp32.  ``state`` (and slot_idx) receives the
+    strided; h0, s_final [N, D] fp32.  Gates that grow must not sum to 88 or more
+    within a chunk of 16 tokens.  ``state`` (and slot_idx) receives the
     decode state of every sequence; want_carry=True returns the fp32 rows that
     glr_backward needs.  Returns (h, s_final, carry, error word)."""
     c = _Call("gdn_glr_forward", x, stream)

@@ -231,3 +231,39 @@ def test_a_long_sequence_among_short_ones_is_not_walked_by_one_thread(gdn):
     rows = slice(40, 40 + L)
     alone = best(x[rows], g[rows], dh[rows], h0[:1], ds[:1], W.cu_seqlens_of([L], "cuda"))
     assert among[0] < 4 * alone[0] and among[1] < 4 * alone[1], (among, alone)
+
+
+@pytest.mark.parametrize("complement", [False, True])
+@pytest.mark.parametrize("lens,D", [([40], 64), ([40], 33), ([40] * 64, 256)])
+def test_gates_that_grow_up_to_the_stated_sum(gdn, lens, D, complement):
+    """A chunk whose gates sum to 88 (A = 1.65e38), one that takes it back, then a
+    reset: exact within the bounds, states of zero stay zero, and the decode steps
+    follow."""
+    N, L = len(lens), lens[0]
+    g = torch.zeros((L, D))
+    g[:16], g[16:32], g[32:] = 5.5, -5.5, -0.5
+    g[36] = float("-inf")
+    g = g.repeat(N, 1).cuda()
+    x = torch.zeros_like(g)
+    h0 = torch.linspace(-1e-3, 1e-3, N * D).reshape(N, D).cuda()
+    h0[:, 5] = 0
+    x[:, 7:] = h0.repeat_interleave(L, 0)[:, 7:]
+    cu = W.cu_seqlens_of(lens, "cuda")
+    h, fin, carry, err = gdn.glr_forward(x, g, cu, h0=h0, complement=complement, want_carry=True)
+    ok(gdn, err)
+    args = (f64(x), f64(g), lens, f64(h0), complement)
+    assert not h[:, 5].any() and not fin[:, 5].any()
+    close(h, glr.forward(*args)[0], glr.forward_bound(*args)[0])
+    dh = torch.zeros_like(x)
+    dh[::7] = 1
+    grads, err = gdn.glr_backward(x, g, cu, carry, dh, complement=complement)
+    ok(gdn, err)
+    args = (*args[:3], f64(dh), f64(h0), None, complement)
+    for got, w, b in zip(grads.values(), glr.backward(*args), glr.backward_bound(*args)):
+        close(got, w, b)
+    state = gdn.GlrDecodeState(N, D)
+    state.h.copy_(h0)
+    first = cu[:-1].long()
+    for t in range(L):
+        step = gdn.glr_decode_step(state, x[first + t], g[first + t], complement=complement)
+        assert torch.equal(step, h[first + t]), t
