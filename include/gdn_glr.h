@@ -95,8 +95,11 @@ int64_t gdn_glr_carry_rows(int n_seqs, int64_t total_tokens);
  * carry       [gdn_glr_carry_rows, D] fp32 or NULL: the states at the tile
  *             starts, which gdn_glr_backward needs
  * error_word  optional device int32 (4-byte aligned), cleared by the call;
- *             invalid cu_seqlens set GDN_DEVERR_CU_SEQLENS there and leave
- *             the offending sequences' outputs unwritten.
+ *             invalid cu_seqlens set GDN_DEVERR_CU_SEQLENS there.  A sequence
+ *             that ends before it starts, or leaves the batch, is not
+ *             written; what the call's outputs hold for the others, which
+ *             may overlap then, is not specified.  Nothing but the outputs is
+ *             written.
  * A forward over a prefix whose length is a multiple of GDN_GLR_CHUNK,
  * followed by one over the rest with h0 = s_final, gives the bits of one
  * forward over the whole.  n_seqs may be 0 and sequences may be empty.

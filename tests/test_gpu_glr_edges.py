@@ -267,3 +267,59 @@ def test_gates_that_grow_up_to_the_stated_sum(gdn, lens, D, complement):
     for t in range(L):
         step = gdn.glr_decode_step(state, x[first + t], g[first + t], complement=complement)
         assert torch.equal(step, h[first + t]), t
+
+
+@pytest.mark.parametrize("lens,D", [([40, 0, 60], 96), ([40, 0, 60], 97),     # tiles
+                                    ([9, 5] * 60, 512), ([9, 5] * 60, 257),   # short
+                                    ([3] * 50 + [1500] + [2] * 50, 512)])     # both
+@pytest.mark.parametrize("how", ["overlap", "falls", "starts late", "ends early", "ends late",
+                                 "negative", "far out", "all alike"])
+def test_invalid_cu_seqlens_are_reported_and_stay_inside(gdn, lens, D, how):
+    """The error word is set, nothing around the outputs is written, and the next call
+    clears the word and is right."""
+    x, g, dh, h0, ds, cu = draw(lens, D, 84)
+    T, N = x.shape[0], len(lens)
+    bad = cu.tolist()
+    m = max(2, N // 2)
+    if how == "overlap":    # (at an edge behind a sequence that has tokens: not valid)
+        assert bad[m - 1] > 0
+        bad[m] = 0
+    elif how == "falls":
+        bad[m] = bad[m + 1] + 1
+    elif how == "starts late":
+        bad[0] = 1
+    elif how == "ends early":
+        bad[N] = T - 1
+    elif how == "ends late":
+        bad[N] = T + 1
+    elif how == "negative":
+        bad[1] = -5
+    elif how == "far out":
+        bad[m] = 2 ** 31 - 1
+    else:
+        bad = [T // 2] * (N + 1)
+    bad = torch.tensor(bad, dtype=torch.int32, device="cuda")
+
+    def guarded(shape, dtype):
+        whole = torch.full((shape[0] + 4, shape[1]), 7.0, dtype=dtype, device="cuda")
+        return whole, whole[2:-2]
+    rows = gdn.glr_carry_rows(N, T)
+    bufs = [guarded(s, d) for s, d in (((T, D), BF), ((N, D), F32), ((rows, D), F32),
+                                       ((T, D), BF), ((T, D), F32), ((N, D), F32))]
+    h, fin, carry, dx, dg, dh0 = (b[1] for b in bufs)
+    state = gdn.GlrDecodeState(N, D)
+    carry.zero_()   # (the rows of sequences that are left out are read by the backward)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdn.glr_forward(x, g, bad, h0=h0, h=h, s_final=fin, carry=carry, state=state, error=err)
+    assert gdn.check_error(err) == gdn.GDN_DEVERR_CU_SEQLENS
+    err.zero_()
+    gdn.glr_backward(x, g, bad, carry, dh, ds_final=ds, error=err,
+                     grads={"dx": dx, "dg": dg, "dh0": dh0})
+    assert gdn.check_error(err) == gdn.GDN_DEVERR_CU_SEQLENS
+    for whole, _ in bufs:
+        assert (whole[:2] == 7).all() and (whole[-2:] == 7).all()
+    assert state.pos.min() >= 0 and state.pos.max() < 16
+    want = gdn.glr_forward(x, g, cu, h0=h0)[0]
+    gdn.glr_forward(x, g, cu, h0=h0, h=h, s_final=fin, carry=carry, error=err)
+    ok(gdn, err)
+    assert torch.equal(h, want)
