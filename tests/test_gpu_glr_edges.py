@@ -323,3 +323,78 @@ def test_invalid_cu_seqlens_are_reported_and_stay_inside(gdn, lens, D, how):
     gdn.glr_forward(x, g, cu, h0=h0, h=h, s_final=fin, carry=carry, error=err)
     ok(gdn, err)
     assert torch.equal(h, want)
+
+
+@pytest.mark.parametrize("D", [64, 63])
+@pytest.mark.parametrize("L", [5000, 129])
+def test_a_sequence_alone_has_the_bits_of_any_cluster_size(gdn, L, D):
+    """Alone, a sequence of 64 channels is taken by clusters of 8 blocks forward and 4
+    backward (2 of them for its 129 tokens); among 300 others of 130 tokens by one
+    block, among 49 by two, among 19 of 300 by four or eight.  All outputs, and the
+    oracle for all of them."""
+    x, g, dh, h0, ds, cu = draw([L], D, 85)
+
+    def both(x, g, dh, h0, ds, cu):
+        h, fin, carry, err = gdn.glr_forward(x, g, cu, h0=h0, want_carry=True, out_dtype=F32)
+        ok(gdn, err)
+        grads, err = gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds)
+        ok(gdn, err)
+        return h, fin, grads["dx"], grads["dg"], grads["dh0"]
+
+    alone = both(x, g, dh, h0, ds, cu)
+    for length, n in ((130, 300), (130, 49), (300, 19)):
+        for at in (0, n // 2, n):
+            lens = [length] * at + [L] + [length] * (n - at)
+            others = draw(lens, D, 86)[:5]
+            start = length * at
+            for mine, t in zip((x, g, dh), others):
+                t[start:start + L] = mine
+            others[3][at], others[4][at] = h0[0], ds[0]
+            got = both(*others, W.cu_seqlens_of(lens, "cuda"))
+            rows = slice(start, start + L)
+            want = (got[0][rows], got[1][at:at + 1], got[2][rows], got[3][rows],
+                    got[4][at:at + 1])
+            assert all(torch.equal(a, b) for a, b in zip(alone, want)), (length, n, at)
+    args = (f64(x), f64(g), [L])
+    for got, w, b in zip(alone[:2], glr.forward(*args, f64(h0)),
+                         glr.forward_bound(*args, f64(h0))):
+        close(got, w, b)
+    want = glr.backward(*args, f64(dh), f64(h0), f64(ds))
+    bound = list(glr.backward_bound(*args, f64(dh), f64(h0), f64(ds)))
+    bound[0] = bound[0] + 2.0 ** -8 * (np.abs(want[0]) + bound[0])
+    for got, w, b in zip(alone[2:], want, bound):
+        close(got, w, b)
+
+
+@pytest.mark.parametrize("complement", [False, True])
+@pytest.mark.parametrize("lens,D", [([130, 20, 300], 64), ([130, 20, 300], 61), ([5000, 3], 64),
+                                    ([5, 20, 17] * 40, 512),
+                                    ([3, 2] * 40 + [1300] + [2] * 40, 512)])
+def test_what_lies_behind_a_sequence_does_not_matter(gdn, lens, D, complement):
+    """NaN and infinities in every second sequence, which a tile's copies bring in with
+    the first's last tokens, in the rows behind the batch and in the columns beside it."""
+    x, g, dh, h0, ds, cu = draw(lens, D, 87)
+    edges = cu.tolist()
+    T = edges[-1]
+    kw = dict(complement=complement)
+
+    def both(x, g, dh):
+        h, fin, carry, err = gdn.glr_forward(x, g, cu, h0=h0, want_carry=True, **kw)
+        ok(gdn, err)
+        grads, err = gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds, **kw)
+        ok(gdn, err)
+        return (h, grads["dx"], grads["dg"]), (fin, grads["dh0"])
+
+    want_tok, want_seq = both(x, g, dh)
+    wide = []
+    for t, junk in ((x, float("nan")), (g, float("nan")), (dh, float("inf"))):
+        w = torch.full((T + 140, D + 64), junk, dtype=t.dtype, device="cuda")
+        w[:T, 16:16 + D] = t
+        for n in range(1, len(lens), 2):
+            w[edges[n]:edges[n + 1]] = junk
+        wide.append(w[:T, 16:16 + D])
+    tok, seq = both(*wide)
+    for n in range(0, len(lens), 2):
+        rows = slice(edges[n], edges[n + 1])
+        assert all(torch.equal(a[rows], b[rows]) for a, b in zip(tok, want_tok)), n
+        assert all(torch.equal(a[n], b[n]) for a, b in zip(seq, want_seq)), n
