@@ -398,3 +398,86 @@ def test_what_lies_behind_a_sequence_does_not_matter(gdn, lens, D, complement):
         rows = slice(edges[n], edges[n + 1])
         assert all(torch.equal(a[rows], b[rows]) for a, b in zip(tok, want_tok)), n
         assert all(torch.equal(a[n], b[n]) for a, b in zip(seq, want_seq)), n
+
+
+@pytest.mark.parametrize("D", [64, 63])
+def test_offsets_beyond_32_bits(gdn, D):
+    """Rows 2^20 elements apart: from row 2048 on an element's offset passes 2^31, in the
+    inputs and in the outputs."""
+    T, lens = 2100, [900, 1200]
+    wide = torch.empty((T, 1 << 20), dtype=BF, device="cuda")
+    x, g, dh, h0, ds, cu = draw(lens, D, 88, gt=BF)
+    cols = [wide[:, 64 * i:64 * i + D] for i in range(6)]
+    for c, t in zip(cols, (x, g, dh)):
+        c.copy_(t)
+    for c in cols[3:]:
+        c.fill_(7)
+    h, fin, carry, err = gdn.glr_forward(x, g, cu, h0=h0, want_carry=True)
+    grads, _ = gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds)
+    got, fin2, carry2, err = gdn.glr_forward(cols[0], cols[1], cu, h0=h0, h=cols[3],
+                                             want_carry=True)
+    ok(gdn, err)
+    out, err = gdn.glr_backward(cols[0], cols[1], cu, carry2, cols[2], ds_final=ds,
+                                grads={"dx": cols[4], "dg": cols[5]})
+    ok(gdn, err)
+    assert torch.equal(got, h) and torch.equal(fin2, fin)
+    assert all(torch.equal(out[k], grads[k]) for k in grads)
+
+
+def test_decode_slots_beyond_32_bits(gdn):
+    """A slot of 2^20 channels whose elements lie behind 2^31 others."""
+    D, n = 1 << 20, 2060
+    state = gdn.GlrDecodeState(n, D)
+    small = gdn.GlrDecodeState(2, D)
+    x, g, _, h0, _, _ = draw([2], D, 89)
+    slots = torch.tensor([n - 1, 0], dtype=torch.int32, device="cuda")
+    state.h[slots.long()] = h0.expand(2, D)
+    small.h.copy_(h0.expand(2, D))
+    for _ in range(2):
+        a = gdn.glr_decode_step(state, x, g, slot_idx=slots)
+        assert torch.equal(a, gdn.glr_decode_step(small, x, g))
+    ok(gdn, state.error)
+    assert all(torch.equal(big[slots.long()], s) for big, s in zip(state.tensors(),
+                                                                   small.tensors()))
+
+
+@pytest.mark.parametrize("D", [1, 2, 6, 30, 34])
+def test_narrow_rows_of_a_wide_buffer(gdn, D):
+    """Rows that start on 16 bytes, with fewer channels than a slab or a few more."""
+    lens = [300, 1, 140]
+    x, g, dh, h0, ds, cu = draw(lens, D, 90)
+    T = x.shape[0]
+    wide = [torch.full((T, 64), float("nan"), dtype=t.dtype, device="cuda") for t in (x, g, dh)]
+    for w, t in zip(wide, (x, g, dh)):
+        w[:, 8:8 + D] = t
+    a = [w[:, 8:8 + D] for w in wide]
+    h, fin, carry, err = gdn.glr_forward(a[0], a[1], cu, h0=h0, want_carry=True, out_dtype=F32)
+    ok(gdn, err)
+    grads, err = gdn.glr_backward(a[0], a[1], cu, carry, a[2], ds_final=ds)
+    ok(gdn, err)
+    args = (f64(x), f64(g), lens)
+    for got, w, b in zip((h, fin), glr.forward(*args, f64(h0)),
+                         glr.forward_bound(*args, f64(h0))):
+        close(got, w, b)
+    want = glr.backward(*args, f64(dh), f64(h0), f64(ds))
+    bound = list(glr.backward_bound(*args, f64(dh), f64(h0), f64(ds)))
+    bound[0] = bound[0] + 2.0 ** -8 * (np.abs(want[0]) + bound[0])
+    for got, w, b in zip((grads["dx"], grads["dg"], grads["dh0"]), want, bound):
+        close(got, w, b)
+
+
+def test_some_of_a_longer_list_of_sequences(gdn):
+    """n_seqs sequences at the front of a longer cu_seqlens."""
+    x, g, dh, h0, ds, cu = draw([50, 7, 300, 20], 64, 91)
+    T = 57
+    h, fin, carry, err = gdn.glr_forward(x, g, cu, h0=h0, want_carry=True)
+    part, fin2, carry2, err = gdn.glr_forward(x[:T], g[:T], cu, n_seqs=2, h0=h0[:2],
+                                              want_carry=True)
+    ok(gdn, err)
+    assert torch.equal(part, h[:T]) and torch.equal(fin2, fin[:2])
+    grads, err = gdn.glr_backward(x, g, cu, carry, dh, ds_final=ds)
+    some, err = gdn.glr_backward(x[:T], g[:T], cu, carry2, dh[:T], n_seqs=2, ds_final=ds[:2])
+    ok(gdn, err)
+    assert torch.equal(some["dg"], grads["dg"][:T]) and torch.equal(some["dh0"], grads["dh0"][:2])
+    with pytest.raises(ValueError, match="entries"):
+        gdn.glr_forward(x, g, cu, n_seqs=5)

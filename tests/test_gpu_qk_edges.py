@@ -74,3 +74,24 @@ def test_fp32_heads_without_a_rotation(gdn, T, Hq, Hk, d, out):
         if out == BF:
             bound = bound + 2.0 ** -8 * (np.abs(want) + bound)
         assert y.dtype == out and (np.abs(f64(y) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_offsets_beyond_32_bits(gdn, d):
+    """Tokens 2^20 elements apart: from token 2048 on an element's offset passes 2^31."""
+    T, Hq, Hk = 2100, 2, 1
+    wide = torch.empty((T, 1 << 20), dtype=BF, device="cuda")
+    q, k, doq, dok, wq, wk = draw(T, Hq, Hk, d, 6, gdt=BF)
+    views, at = [], 0
+    for t in (q, k, doq, dok, q, k, q, k):
+        views.append(wide[:, at:at + t.shape[1] * d].unflatten(1, (t.shape[1], d)))
+        at += t.shape[1] * d
+        views[-1].copy_(t)
+    kw = dict(norm="rms", wq=wq, wk=wk, positions=torch.arange(T, dtype=torch.int32).cuda(),
+              inv_freq=torch.rand(d // 4).cuda())
+    oq, ok = gdn.qk_norm_forward(q, k, **kw)
+    a, b = gdn.qk_norm_forward(views[0], views[1], oq=views[4], ok=views[5], **kw)
+    assert torch.equal(a, oq) and torch.equal(b, ok)
+    want = gdn.qk_norm_backward(q, k, doq, dok, **kw)
+    got = gdn.qk_norm_backward(*views[:4], grads={"dq": views[6], "dk": views[7]}, **kw)
+    assert all(torch.equal(got[s], want[s]) for s in want)
