@@ -22,11 +22,11 @@
 // the state over all of them.  The data are still read once.
 //
 // What bounds it is memory: 8 bytes an element forward (bf16 x and h, fp32 g) and
-// 14 backward, for 18 and 29 instructions per 32 elements.  16384 x 2048 in 32
-// sequences: 48 us (5.6 TB/s) and 77 us (6.1 TB/s, of 6.5 that a copy reaches);
-// 57344 x 4096 in 64 uneven ones: 310 and 591 us (6.1 and 5.6 TB/s).  A sequence
+// 14 backward, for 21 and 33 instructions per 32 elements.  16384 x 2048 in 32
+// sequences: 48 us (5.5 TB/s) and 78 us (6.0 TB/s, of 6.5 that a copy reaches);
+// 57344 x 4096 in 64 uneven ones: 300 and 574 us (6.3 and 5.7 TB/s).  A sequence
 // alone is bound by its steps, one after the other: 65536 x 2048 with bf16 gates
-// takes 181 and 255 us (4.4 and 5.3 TB/s), 32768 x 1024 73 and 118.  Chunks of 16
+// takes 181 and 263 us (4.4 and 5.1 TB/s), 32768 x 1024 73 and 119.  Chunks of 16
 // tokens keep the maps of two channels (64 floats) in a thread's registers from
 // the fold to the write, at three blocks of a multiprocessor; slabs of 32
 // channels make a token's row of a box a whole 128-byte line of fp32.
@@ -131,7 +131,7 @@ __device__ __forceinline__ float decay_far(float g) {
 // below 1 (1.4 U above), and half a step alone for g towards 0, without a bias
 // (ex2.approx: 2.3 U and a bias of -0.3 U measured over [-1/2, 0], expf 2.3 and
 // +0.2).  Two gates at a time, packed: forward and backward of 65536 x 2048
-// alone 446 us (433 without it), of 10240 x 2048 in 5 uneven sequences 96 (95).
+// alone 444 us (430 without it), of 10240 x 2048 in 5 uneven sequences 95 (92).
 // expf, exact to 2 U everywhere, takes 490 and 98.
 __device__ __forceinline__ float2 decay_near(float2 g) {
   float2 s = f2(1.f / 120.f, 1.f / 120.f);
@@ -495,8 +495,8 @@ __device__ __forceinline__ float glr_chain(const float2* maps, float z, int lane
 //
 // Direct (rows that a tensor map cannot describe: a base or stride off 16
 // bytes, an odd width): loads from global memory, all of the chunk's at once,
-// one element a thread (20000 x 999 in 9 sequences: 58 and 103 us; the same of
-// 1000 channels, staged: 42 and 60).
+// one element a thread (20000 x 999 in 9 sequences: 58 and 104 us; the same of
+// 1000 channels, staged: 40 and 60).
 template <class T, int V, bool STAGED>
 struct GlrSource;
 
@@ -1143,7 +1143,8 @@ __global__ void __launch_bounds__(kGlrShortThreads) k_glr_short_backward(const G
 
 // One block per row (a row's pos is read and written by one block).  A row's
 // first channels are loaded beside its pos, not behind it.  256 rows of 4096
-// channels are 29 MB: 4.7 us in a graph, 6.2 TB/s; one row 2.5 us.
+// channels take 5.2 us a step in a graph of steps (their 29 MB stay in the L2), one
+// of 2048 1.9.
 constexpr int kGlrStepThreads = 1024;
 
 template <class IN, class G, class OUT, int V, int MODE>
@@ -1215,22 +1216,24 @@ constexpr size_t kGlrStatic = 4608;  // shared memory of a block that its launch
 
 // Launch shape.  Blocks of a cluster: doubled while every block of the grid
 // still has a place on the device and a sequence has tiles for them on average
-// (65536 x 2048 alone, forward: 373, 252, 178 us with 1, 2 and 4; 8 have no
-// place and took 303).  A backward step of 8 blocks is slower than two of 4
-// (32768 x 1024: 131 against 115 us).
+// (65536 x 2048 alone, forward: 387, 256, 183 us with 1, 2 and 4; 8 have no
+// place and take 307).  A backward step of 8 blocks is slower than two of 4
+// (32768 x 1024: 212 against 119 us).
 //
 // Stages: as many as the shared memory of a multiprocessor holds for the blocks
 // that it gets, and at least two.  A backward cluster would rather have three
 // and fewer blocks: with two its copies start only behind the last step (20000
-// x 1000 in 9 sequences: 84 against 72 us); where blocks are many the others
-// cover that, and three blocks with two stages win (16384 x 2048 in 32: 90
-// against 107 us).
+// x 1000 in 9 sequences with bf16 gates: 72 against 55 us, 10240 x 2048 in 5 61
+// against 55; of fp32 data the latter takes 81 against 89, and with fp32 gates
+// two blocks are all that fit in either case).  Where blocks are many the others
+// cover that, and three blocks with two stages win (16384 x 2048 in 32: 78
+// against 84 us, of the complement form 86 against 100).
 //
 // Longest sequences first where some blocks have to wait for a place: 10240
 // tokens of 2048 channels in sequences of 531, 793, 1762, 2136 and 5018, forward
-// and backward: 92 us (without it 115); where it gains nothing, 16384 x 2048 in
-// 32 equal ones: 145 (141).  With 64 sequences every block's search for its own
-// cost more than the order gained (57344 x 4096: 913 against 900 us).
+// and backward: 95 us (without it 102); where it gains nothing, 16384 x 2048 in
+// 32 equal ones: 129 (125).  With 64 sequences every block's search for its own
+// costs more than the order gains.
 struct GlrShape {
   int cs, stages;
   bool longest_first;
@@ -1257,10 +1260,10 @@ static GlrShape glr_shape(const GlrArgs& p, size_t stage, int most, bool backwar
     sh.cs *= 2;
   // Sequences of unequal length keep the device waiting for the longest: two
   // blocks for each then gain more than a second wave of blocks costs (10240
-  // tokens of 2048 channels in 5 sequences, forward and backward: 92 against 145
-  // us where they are uneven, 100 against 88 us where they are equal), for a
-  // backward from a few more units on (20000 x 2048 in 9, uneven: 104 against 133
-  // us, 18432 in 9 equal ones: 94 against 104; the forward the same within 2 us).
+  // tokens of 2048 channels in 5 sequences, forward and backward: 95 against 148
+  // us where they are uneven, 103 against 86 us where they are equal), for a
+  // backward from a few more units on (20000 x 2048 in 9, uneven: 104 against 134
+  // us, 18432 in 9 equal ones: 95 against 104; the forward the same within 2 us).
   const int waves = backward && stage > 0 ? 4 : most;
   if (sh.cs == 1 && seqs > 1 && units <= waves * kSms && p.T > (int64_t)seqs * kGlrTile)
     sh.cs = 2;
@@ -1353,7 +1356,7 @@ static cudaError_t glr_launch(GlrOp op, GlrArgs& p, bool pairs, cudaStream_t st)
   }
   // Sequences of up to 64 tokens on average, and more of them than one wave of
   // tile blocks takes: 64 sequences of 4096 channels, forward and backward, 300
-  // tokens: 35 us (tiles: 130), 4096: 132 (161), 8192: 238 (207).
+  // tokens: 33 us (tiles: 133), 4096: 132 (166), 8192: 249 (213).
   if (p.T > (int64_t)64 * p.N || (int64_t)p.N * p.slabs <= 3 * 148)
     return glr_tiles<IN, G, OUT, MODE>(op, p, pairs, st);
   // The average says nothing of the longest, and a thread that walks thousands of
